@@ -56,9 +56,6 @@
 namespace gdn {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kC = 32;     // tokens per chunk
 constexpr int kNCT = 2;    // 16-token tiles per chunk
 constexpr int kPrep = 6;   // prep waves per workgroup (four compute, two load)
@@ -107,49 +104,6 @@ struct Lay {
   static_assert(kC * DVT * 2 % 1024 == 0, "V tile must be whole KiB");
   static_assert(TOTAL <= 160 * 1024, "LDS budget");
 };
-
-__device__ __forceinline__ uint32_t lds_addr(const void *p) {
-  // generic -> LDS address-space conversion yields the 32-bit LDS offset
-  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
-      (const __attribute__((address_space(3))) char *)(p)));
-}
-
-// Raw buffer resource over [base, base + bytes): loads at or past the end
-// return zeros, stores there are dropped.
-__device__ __forceinline__ i32x4 buffer_rsrc(const void *base, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(base);
-  i32x4 r;
-  r[0] = static_cast<int32_t>(static_cast<uint32_t>(a));
-  r[1] = static_cast<int32_t>(static_cast<uint32_t>(a >> 32));  // stride 0
-  r[2] = static_cast<int32_t>(bytes);
-  r[3] = 0x00020000;  // raw dword access
-  return r;
-}
-
-// Direct-to-LDS loads: lane L's data lands at (M0 + 16*L) or (M0 + 4*L).
-// Written in asm so the compiler does not serialise later LDS reads behind
-// them; completion is tracked explicitly with vmcnt waits. M0 is written one
-// wait state before the load reads it.
-__device__ __forceinline__ void dma16(const i32x4 &rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               ::"v"(voff), "s"(rsrc), "s"(lds)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const i32x4 &rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               ::"v"(voff), "s"(rsrc), "s"(lds)
-               : "memory", "m0");
-}
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  static_assert(N >= 0 && N < 64, "vmcnt range");
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-// workgroup barrier that does not drain outstanding direct-to-LDS loads
-__device__ __forceinline__ void wg_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
 
 template <int N>
 __device__ __forceinline__ float dpp_shr(float x) {

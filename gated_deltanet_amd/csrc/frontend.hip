@@ -27,58 +27,6 @@ namespace {
 constexpr int kTaps = 4;
 constexpr int kRowsPerBlock = 64;  // output gate rows per workgroup
 
-template <typename T>
-struct Vec8;
-template <>
-struct Vec8<float> {
-  __device__ static void load(const float *p, float *o) {
-    const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
-    const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = a[i];
-      o[4 + i] = b[i];
-    }
-  }
-  __device__ static void store(float *p, const float *v) {
-    f32x4 a, b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = v[i];
-      b[i] = v[4 + i];
-    }
-    *reinterpret_cast<f32x4 *>(p) = a;
-    *reinterpret_cast<f32x4 *>(p + 4) = b;
-  }
-};
-template <>
-struct Vec8<_Float16> {
-  __device__ static void load(const _Float16 *p, float *o) { io<_Float16>::load16(p, o); }
-  __device__ static void store(_Float16 *p, const float *v) {
-    f16x8 r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = (_Float16)v[i];
-    *reinterpret_cast<f16x8 *>(p) = r;
-  }
-};
-template <>
-struct Vec8<bf16_t> {
-  __device__ static void load(const bf16_t *p, float *o) { io<bf16_t>::load16(p, o); }
-  __device__ static void store(bf16_t *p, const float *v) {
-    typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-    bf16x8_t r;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[i];  // round to nearest even
-    *reinterpret_cast<bf16x8_t *>(p) = r;
-  }
-};
-
-// 1 / (1 + exp(-x)) with one v_exp_f32 and one v_rcp_f32 (about 1 ulp each);
-// exp overflows to inf for x < -88 and the reciprocal then gives 0
-__device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
-}
-
 // index of the sequence containing `row` of a packed batch: the last k with
 // cu[k] <= row (0 if none). Called with a row that is uniform across the
 // workgroup, so the loads go through the scalar cache.

@@ -11,6 +11,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // bf16 is carried as its 16 raw bits.
 typedef uint16_t bf16_t;
@@ -71,6 +73,101 @@ struct io<_Float16> {
   __device__ static __forceinline__ float to_f32(_Float16 x) { return static_cast<float>(x); }
   __device__ static __forceinline__ _Float16 from_f32(float x) { return static_cast<_Float16>(x); }
 };
+
+// Eight consecutive elements as fp32, one or two 16-byte accesses.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<float> {
+  __device__ static void load(const float *p, float *o) {
+    const f32x4 a = *reinterpret_cast<const f32x4 *>(p);
+    const f32x4 b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = a[i];
+      o[4 + i] = b[i];
+    }
+  }
+  __device__ static void store(float *p, const float *v) {
+    f32x4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = v[i];
+      b[i] = v[4 + i];
+    }
+    *reinterpret_cast<f32x4 *>(p) = a;
+    *reinterpret_cast<f32x4 *>(p + 4) = b;
+  }
+};
+template <>
+struct Vec8<_Float16> {
+  __device__ static void load(const _Float16 *p, float *o) { io<_Float16>::load16(p, o); }
+  __device__ static void store(_Float16 *p, const float *v) {
+    f16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (_Float16)v[i];
+    *reinterpret_cast<f16x8 *>(p) = r;
+  }
+};
+template <>
+struct Vec8<bf16_t> {
+  __device__ static void load(const bf16_t *p, float *o) { io<bf16_t>::load16(p, o); }
+  __device__ static void store(bf16_t *p, const float *v) {
+    bf16x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = (__bf16)v[i];  // round to nearest even
+    *reinterpret_cast<bf16x8 *>(p) = r;
+  }
+};
+
+// 1 / (1 + exp(-x)) with one v_exp_f32 and one v_rcp_f32 (about 1 ulp each);
+// exp overflows to inf for x < -88 and the reciprocal then gives 0
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+}
+
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  // generic -> LDS address-space conversion yields the 32-bit LDS offset
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (const __attribute__((address_space(3))) char *)(p)));
+}
+
+// Raw buffer resource over [base, base + bytes): loads at or past the end
+// return zeros, stores there are dropped.
+__device__ __forceinline__ i32x4 buffer_rsrc(const void *base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  i32x4 r;
+  r[0] = static_cast<int32_t>(static_cast<uint32_t>(a));
+  r[1] = static_cast<int32_t>(static_cast<uint32_t>(a >> 32));  // stride 0
+  r[2] = static_cast<int32_t>(bytes);
+  r[3] = 0x00020000;  // raw dword access
+  return r;
+}
+
+// Direct-to-LDS loads: lane L's data lands at (M0 + 16*L) or (M0 + 4*L).
+// Written in asm so the compiler does not serialise later LDS reads behind
+// them; completion is tracked explicitly with vmcnt waits. M0 is written one
+// wait state before the load reads it.
+__device__ __forceinline__ void dma16(const i32x4 &rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               ::"v"(voff), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(const i32x4 &rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               ::"v"(voff), "s"(rsrc), "s"(lds)
+               : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// workgroup barrier that does not drain outstanding direct-to-LDS loads
+__device__ __forceinline__ void wg_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 // ---------------------------------------------------------------------------
 // MFMA fragments.
