@@ -21,6 +21,17 @@ Functions carry the names of the C entry points declared in include/gdn.h:
   cu_seqlens=None, out_dtype=None, ...)`` -> (y, S_T)
 * ``gdn_chunk_fwd_segmented_workspace_size(rows, N, H, dk, dv, segments,
   in_dtype)`` -> bytes
+
+The layer around the mixer:
+
+* ``gdn_add_rmsnorm(x, norm_w=None, residual=None, rms_eps=1e-6,
+  out_dtype=None)`` -> (y, r, y_scale)
+* ``gdn_add_rmsnorm_bwd(dy, r, norm_w=None, dr=None, rms_eps=1e-6)`` ->
+  (dx, dnorm_w)
+* ``gdn_quantize_rows(x)`` -> (y, y_scale)
+* ``gdn_linear(x, w, bias=None, residual=None, act="none", out_dtype=None,
+  x_scale=None, w_scale=None, want_pre=False)`` -> (y, pre)
+* ``gdn_linear_bwd(dy, x, w, pre=None, act="none")`` -> (dx, dw, dbias)
 """
 from __future__ import annotations
 
@@ -35,7 +46,10 @@ LIB_PATH = os.path.join(_HERE, "libgdn.so")
 GDN_F32 = 0
 GDN_BF16 = 1
 GDN_F16 = 2
+GDN_E4M3 = 3
 GDN_OK = 0
+# activations of gdn_linear (gdn_act_e)
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}
 
 _lib = None
 
@@ -103,6 +117,25 @@ def load_library(path: str = LIB_PATH):
     lib.gdn_chunk_fwd_segmented_noalloc.argtypes = [vp, vp, vp, fp, fp, fp, vp, fp, ip, i32, i32,
                                                     i32, i32, i32, i32, i32, i32, vp]
     lib.gdn_chunk_fwd_segmented_noalloc.restype = ctypes.c_int
+    lib.gdn_add_rmsnorm.argtypes = [vp, vp, fp, f32, vp, vp, fp, i64, i32, i32, i32, vp]
+    lib.gdn_add_rmsnorm.restype = ctypes.c_int
+    lib.gdn_quantize_rows.argtypes = [vp, vp, fp, i64, i32, i32, vp]
+    lib.gdn_quantize_rows.restype = ctypes.c_int
+    lib.gdn_add_rmsnorm_bwd_workspace_size.argtypes = [i64, i32]
+    lib.gdn_add_rmsnorm_bwd_workspace_size.restype = sz
+    lib.gdn_add_rmsnorm_bwd.argtypes = [vp, vp, vp, fp, f32, vp, fp, i64, i32, i32, i32, vp, sz,
+                                        vp]
+    lib.gdn_add_rmsnorm_bwd.restype = ctypes.c_int
+    lib.gdn_linear_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.gdn_linear_workspace_size.restype = sz
+    lib.gdn_linear.argtypes = [vp, fp, vp, fp, fp, vp, vp, vp, i64, i32, i32, i32, i32, i32, vp,
+                               sz, vp]
+    lib.gdn_linear.restype = ctypes.c_int
+    lib.gdn_linear_bwd_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32]
+    lib.gdn_linear_bwd_workspace_size.restype = sz
+    lib.gdn_linear_bwd.argtypes = [vp, vp, vp, vp, vp, vp, fp, i64, i32, i32, i32, i32, i32, vp,
+                                   sz, vp]
+    lib.gdn_linear_bwd.restype = ctypes.c_int
     lib.gdn_status_string.argtypes = [ctypes.c_int]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_last_error.argtypes = []
@@ -853,6 +886,248 @@ def gdn_chunk_fwd_fused(q_raw, k_raw, v_raw, conv_w, log_alpha, beta, z, S0=None
                                  workspace.numel() * workspace.element_size(), _stream(dev))
     _check(rc, lib, "gdn_chunk_fwd_fused")
     return o, S_T
+
+
+def _dt8(t: torch.dtype) -> int:
+    return GDN_E4M3 if t == torch.float8_e4m3fn else _dt(t)
+
+
+def _rows_d(x, name):
+    """(rows, d) of a tensor [..., d]."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise GdnError("%s must be [..., d] with d >= 1" % name)
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def _vector(t, name, n):
+    """An optional fp32 vector of n values."""
+    if t is not None:
+        _need(t, name, torch.float32)
+        _shape(t, name, (n,))
+
+
+def _like(t, name, shape, dtype):
+    """An optional tensor of this shape and dtype."""
+    if t is not None:
+        _need(t, name, dtype)
+        _shape(t, name, shape)
+
+
+def _workspace(workspace, need, dev):
+    """(workspace, bytes): the caller's, or one allocated here when needed."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _launch(lib, name, dev, *args):
+    """Call a C entry point on dev's current stream, with dev current (kernels
+    launch on the current device)."""
+    fn = getattr(lib, name)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(dev))
+    _check(rc, lib, name)
+
+
+def gdn_add_rmsnorm(x, norm_w=None, residual=None, rms_eps=1e-6, out_dtype=None, y=None, r=None,
+                    y_scale=None):
+    """r = x + residual, y = r / sqrt(mean(r^2) + eps) * (1 + norm_w) over the
+    last dimension. x, residual [..., d]; norm_w fp32 [d]. out_dtype (default
+    x's) may be torch.float8_e4m3fn: y is then y / y_scale in 8 bits with
+    y_scale fp32 [...], one scale a row. Returns (y, r, y_scale): r is None
+    without a residual (may be passed as x or residual: in place), y_scale None
+    unless y is e4m3."""
+    lib = load_library()
+    _need(x, "x")
+    rows, d = _rows_d(x, "x")
+    in_code = _dt(x.dtype)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    out_code = _dt8(out_dtype)
+    _vector(norm_w, "norm_w", d)
+    _like(residual, "residual", x.shape, x.dtype)
+    _like(y, "y", x.shape, out_dtype)
+    _like(r, "r", x.shape, x.dtype)
+    _like(y_scale, "y_scale", x.shape[:-1], torch.float32)
+    if r is not None and residual is None:
+        raise GdnError("r needs a residual")
+    if y_scale is not None and out_code != GDN_E4M3:
+        raise GdnError("y_scale goes with an e4m3 y")
+    dev = _devices((x, "x"), (norm_w, "norm_w"), (residual, "residual"), (y, "y"), (r, "r"),
+                   (y_scale, "y_scale"))
+    if y is None:
+        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+    if r is None and residual is not None:
+        r = torch.empty_like(x)
+    if y_scale is None and out_code == GDN_E4M3:
+        y_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _launch(lib, "gdn_add_rmsnorm", dev, _p(x), _p(residual), _p(norm_w), float(rms_eps), _p(r),
+            _p(y), _p(y_scale), rows, d, in_code, out_code)
+    return y, r, y_scale
+
+
+def gdn_quantize_rows(x, y=None, y_scale=None):
+    """x [..., d] in 8 bits: (y e4m3 [..., d], y_scale fp32 [...]) with
+    y_scale = max(|row|, 1e-30) / 448 and y = row / y_scale rounded."""
+    lib = load_library()
+    _need(x, "x")
+    rows, d = _rows_d(x, "x")
+    in_code = _dt(x.dtype)
+    _like(y, "y", x.shape, torch.float8_e4m3fn)
+    _like(y_scale, "y_scale", x.shape[:-1], torch.float32)
+    dev = _devices((x, "x"), (y, "y"), (y_scale, "y_scale"))
+    if y is None:
+        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+    if y_scale is None:
+        y_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    _launch(lib, "gdn_quantize_rows", dev, _p(x), _p(y), _p(y_scale), rows, d, in_code)
+    return y, y_scale
+
+
+def gdn_add_rmsnorm_bwd_workspace_size(rows: int, d: int) -> int:
+    return int(load_library().gdn_add_rmsnorm_bwd_workspace_size(rows, d))
+
+
+def gdn_add_rmsnorm_bwd(dy, r, norm_w=None, dr=None, rms_eps=1e-6, want_dnorm_w=True, dx=None,
+                        dnorm_w=None, workspace=None):
+    """Backward of gdn_add_rmsnorm. dy [..., d] (gradient of y, any supported
+    dtype); r [..., d] the forward's r (its x without a residual); dr like r:
+    the gradient that reaches r through the residual stream, or None. Returns
+    (dx, dnorm_w): dx like r (the gradient of x and of the residual; may be
+    passed as dr: in place), dnorm_w fp32 [d] or None."""
+    lib = load_library()
+    _need(r, "r")
+    rows, d = _rows_d(r, "r")
+    in_code = _dt(r.dtype)
+    _need(dy, "dy")
+    _shape(dy, "dy", r.shape)
+    dy_code = _dt(dy.dtype)
+    _vector(norm_w, "norm_w", d)
+    _like(dr, "dr", r.shape, r.dtype)
+    _like(dx, "dx", r.shape, r.dtype)
+    _vector(dnorm_w, "dnorm_w", d)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    dev = _devices((r, "r"), (dy, "dy"), (norm_w, "norm_w"), (dr, "dr"), (dx, "dx"),
+                   (dnorm_w, "dnorm_w"), (workspace, "workspace"))
+    if dx is None:
+        dx = torch.empty_like(r)
+    need = 0
+    if dnorm_w is not None or want_dnorm_w:
+        need = lib.gdn_add_rmsnorm_bwd_workspace_size(rows, d)
+        if dnorm_w is None:
+            dnorm_w = torch.empty(d, dtype=torch.float32, device=dev)
+    workspace, nbytes = _workspace(workspace, need, dev)
+    _launch(lib, "gdn_add_rmsnorm_bwd", dev, _p(dy), _p(r), _p(dr), _p(norm_w), float(rms_eps),
+            _p(dx), _p(dnorm_w), rows, d, in_code, dy_code, _p(workspace), nbytes)
+    return dx, dnorm_w
+
+
+def _act_code(act):
+    try:
+        return ACTIVATIONS[act]
+    except (KeyError, TypeError):
+        raise GdnError("act must be one of %s, not %r" % (sorted(ACTIVATIONS), act)) from None
+
+
+def gdn_linear_workspace_size(M: int, N: int, K: int, in_dtype: torch.dtype) -> int:
+    return int(load_library().gdn_linear_workspace_size(M, N, K, _dt8(in_dtype)))
+
+
+def gdn_linear(x, w, bias=None, residual=None, act="none", out_dtype=None, x_scale=None,
+               w_scale=None, want_pre=False, y=None, pre=None, workspace=None):
+    """y = act(x w^T + bias) + residual. x [..., K] and w [N, K] in fp32, bf16,
+    fp16, or e4m3 with x_scale fp32 [...] and w_scale fp32 [N] (one scale a
+    row); bias fp32 [N]; residual [..., N] in out_dtype (default: x's dtype,
+    bf16 for e4m3 inputs); act "none", "silu", "gelu" or "sigmoid". Returns
+    (y, pre): pre is x w^T + bias in out_dtype with want_pre, for
+    gdn_linear_bwd, else None. y may be passed as residual (in place)."""
+    lib = load_library()
+    _need(x, "x")
+    M, K = _rows_d(x, "x")
+    in_code = _dt8(x.dtype)
+    _need(w, "w", x.dtype)
+    if w.dim() != 2 or w.shape[1] != K or w.shape[0] < 1:
+        raise GdnError("w must be [N, %d], not %s" % (K, tuple(w.shape)))
+    N = w.shape[0]
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if in_code == GDN_E4M3 else x.dtype
+    out_code = _dt(out_dtype)
+    act_code = _act_code(act)
+    if (in_code == GDN_E4M3) != (x_scale is not None) or (x_scale is None) != (w_scale is None):
+        raise GdnError("x_scale and w_scale go with e4m3 inputs")
+    shape = x.shape[:-1] + (N,)
+    _like(x_scale, "x_scale", x.shape[:-1], torch.float32)
+    _vector(w_scale, "w_scale", N)
+    _vector(bias, "bias", N)
+    _like(residual, "residual", shape, out_dtype)
+    _like(y, "y", shape, out_dtype)
+    _like(pre, "pre", shape, out_dtype)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    dev = _devices((x, "x"), (w, "w"), (x_scale, "x_scale"), (w_scale, "w_scale"), (bias, "bias"),
+                   (residual, "residual"), (y, "y"), (pre, "pre"), (workspace, "workspace"))
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype, device=dev)
+    if pre is None and want_pre:
+        pre = torch.empty(shape, dtype=out_dtype, device=dev)
+    workspace, nbytes = _workspace(workspace, lib.gdn_linear_workspace_size(M, N, K, in_code), dev)
+    _launch(lib, "gdn_linear", dev, _p(x), _p(x_scale), _p(w), _p(w_scale), _p(bias),
+            _p(residual), _p(pre), _p(y), M, N, K, act_code, in_code, out_code, _p(workspace),
+            nbytes)
+    return y, pre
+
+
+def gdn_linear_bwd_workspace_size(M: int, N: int, K: int, act: str, in_dtype: torch.dtype,
+                                  dy_dtype: torch.dtype) -> int:
+    return int(load_library().gdn_linear_bwd_workspace_size(M, N, K, _act_code(act),
+                                                            _dt(in_dtype), _dt(dy_dtype)))
+
+
+def gdn_linear_bwd(dy, x, w, pre=None, act="none", want_dx=True, want_dw=True, want_dbias=True,
+                   dx=None, dw=None, dbias=None, workspace=None):
+    """Backward of gdn_linear: du = dy act'(pre), dx = du w, dw = du^T x,
+    dbias = sum of du over rows. dy, pre [..., N] in the forward's out_dtype
+    (pre is needed with an activation); x [..., K], w [N, K] in fp32, bf16 or
+    fp16. Returns (dx, dw, dbias) like x, like w and fp32 [N], None where not
+    wanted. The gradient of the forward's residual is dy."""
+    lib = load_library()
+    _need(x, "x")
+    M, K = _rows_d(x, "x")
+    in_code = _dt(x.dtype)
+    _need(w, "w", x.dtype)
+    if w.dim() != 2 or w.shape[1] != K or w.shape[0] < 1:
+        raise GdnError("w must be [N, %d], not %s" % (K, tuple(w.shape)))
+    N = w.shape[0]
+    _need(dy, "dy")
+    _shape(dy, "dy", x.shape[:-1] + (N,))
+    dy_code = _dt(dy.dtype)
+    act_code = _act_code(act)
+    _like(pre, "pre", dy.shape, dy.dtype)
+    if act_code and pre is None:
+        raise GdnError("act %r needs pre" % act)
+    _like(dx, "dx", x.shape, x.dtype)
+    _like(dw, "dw", w.shape, x.dtype)
+    _vector(dbias, "dbias", N)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    dev = _devices((x, "x"), (w, "w"), (dy, "dy"), (pre, "pre"), (dx, "dx"), (dw, "dw"),
+                   (dbias, "dbias"), (workspace, "workspace"))
+    if dx is None and want_dx:
+        dx = torch.empty_like(x)
+    if dw is None and want_dw:
+        dw = torch.empty_like(w)
+    if dbias is None and want_dbias:
+        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+    workspace, nbytes = _workspace(
+        workspace, lib.gdn_linear_bwd_workspace_size(M, N, K, act_code, in_code, dy_code), dev)
+    _launch(lib, "gdn_linear_bwd", dev, _p(dy), _p(pre), _p(x), _p(w), _p(dx), _p(dw), _p(dbias),
+            M, N, K, act_code, in_code, dy_code, _p(workspace), nbytes)
+    return dx, dw, dbias
 
 
 def gdn_version() -> int:

@@ -973,3 +973,292 @@ GDN_API int gdn_conv_state_from_prefill(const void *q_raw, const void *k_raw, co
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Layer operators around the mixer: norm, row quantiser, matrix product.
+
+namespace {
+
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+
+// no output overlaps an input or another output
+template <size_t NI, size_t NO>
+bool disjoint(const Span (&ins)[NI], const Span (&outs)[NO]) {
+  for (size_t o = 0; o < NO; ++o) {
+    for (size_t i = 0; i < NI; ++i)
+      if (overlap(ins[i].p, ins[i].bytes, outs[o].p, outs[o].bytes)) return false;
+    for (size_t q = o + 1; q < NO; ++q)
+      if (overlap(outs[q].p, outs[q].bytes, outs[o].p, outs[o].bytes)) return false;
+  }
+  return true;
+}
+
+size_t esize_e4m3(int t) { return t == GDN_E4M3 ? 1 : esize(t); }
+
+// rows x d of the norm and the quantiser
+int check_rows(int64_t rows, int32_t d) {
+  if (rows < 0 || d <= 0) return fail(GDN_ERR_INVALID_ARG, "%s", "rows must be >= 0 and d > 0");
+  if (d > gdn::kNormMaxD) return fail(GDN_ERR_UNSUPPORTED, "%s", "d must be at most 32768");
+  if (rows >= (int64_t{1} << 31) || rows * d >= (int64_t{1} << 40))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "input too large");
+  return GDN_OK;
+}
+
+// widest row of a product's operand, in bytes: 256 rows stay within the range
+// of one buffer resource
+constexpr int64_t kLinearMaxPitch = int64_t{1} << 23;
+
+bool linear_sizes_ok(int64_t M, int32_t N, int32_t K, int32_t in_dtype) {
+  const int64_t e = static_cast<int64_t>(esize_e4m3(in_dtype));
+  return M >= 0 && N > 0 && K > 0 && M < (int64_t{1} << 31) && K * e <= kLinearMaxPitch &&
+         N * e <= kLinearMaxPitch && M * N < (int64_t{1} << 40) && M * K < (int64_t{1} << 40);
+}
+
+bool act_ok(int act) { return act >= GDN_ACT_NONE && act <= GDN_ACT_SIGMOID; }
+
+}  // namespace
+
+extern "C" {
+
+GDN_API int gdn_add_rmsnorm(const void *x, const void *residual, const float *norm_w,
+                            float rms_eps, void *r, void *y, float *y_scale, int64_t rows,
+                            int32_t d, int32_t in_dtype, int32_t out_dtype, void *stream) {
+  g_last_error[0] = '\0';
+  const int st = check_rows(rows, d);
+  if (st != GDN_OK) return st;
+  if (!dtype_ok(in_dtype) || !(dtype_ok(out_dtype) || out_dtype == GDN_E4M3))
+    return fail(GDN_ERR_UNSUPPORTED, "%s",
+                "dtypes must be GDN_F32, GDN_BF16 or GDN_F16 (out_dtype also GDN_E4M3)");
+  if (!(rms_eps >= 0.0f)) return fail(GDN_ERR_INVALID_ARG, "%s", "rms_eps must be >= 0");
+  if (rows > 0 && (!x || !y)) return fail(GDN_ERR_INVALID_ARG, "%s", "null input or output pointer");
+  if (rows > 0 && (out_dtype == GDN_E4M3) != (y_scale != nullptr))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "y_scale goes with GDN_E4M3 outputs");
+  if (r && !residual) return fail(GDN_ERR_INVALID_ARG, "%s", "r needs a residual");
+  if (misaligned(x) || misaligned(residual) || misaligned(norm_w) || misaligned(r) ||
+      misaligned(y) || misaligned(y_scale, 4))
+    return fail(GDN_ERR_MISALIGNED, "%s", "tensors and norm_w need 16-byte alignment, y_scale 4");
+  const size_t n = static_cast<size_t>(rows) * d;
+  const size_t ni = n * esize(in_dtype), nw = static_cast<size_t>(d) * 4;
+  const Span outs[3] = {{r, ni}, {y, n * esize_e4m3(out_dtype)}, {y_scale, static_cast<size_t>(rows) * 4}};
+  // r may be x or residual itself: each element is read before it is written
+  const Span ins[3] = {{x == r ? nullptr : x, ni}, {residual == r ? nullptr : residual, ni},
+                       {norm_w, nw}};
+  if (!disjoint(ins, outs)) return fail(GDN_ERR_INVALID_ARG, "%s", "an output overlaps another argument");
+  gdn::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.norm_w = norm_w;
+  a.eps = rms_eps;
+  a.r = r;
+  a.y = y;
+  a.y_scale = y_scale;
+  a.rows = rows;
+  a.d = d;
+  a.in_dtype = in_dtype;
+  a.out_dtype = out_dtype;
+  a.stream = static_cast<hipStream_t>(stream);
+  return hip_status(gdn::launch_add_rmsnorm(a), "gdn_add_rmsnorm launch");
+}
+
+GDN_API int gdn_quantize_rows(const void *x, void *y, float *y_scale, int64_t rows, int32_t d,
+                              int32_t in_dtype, void *stream) {
+  g_last_error[0] = '\0';
+  const int st = check_rows(rows, d);
+  if (st != GDN_OK) return st;
+  if (!dtype_ok(in_dtype))
+    return fail(GDN_ERR_UNSUPPORTED, "%s", "in_dtype must be GDN_F32, GDN_BF16 or GDN_F16");
+  if (rows > 0 && (!x || !y || !y_scale))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "null input or output pointer");
+  if (misaligned(x) || misaligned(y) || misaligned(y_scale, 4))
+    return fail(GDN_ERR_MISALIGNED, "%s", "x and y need 16-byte alignment, y_scale 4");
+  const size_t n = static_cast<size_t>(rows) * d;
+  const Span outs[2] = {{y, n}, {y_scale, static_cast<size_t>(rows) * 4}};
+  const Span ins[1] = {{x, n * esize(in_dtype)}};
+  if (!disjoint(ins, outs)) return fail(GDN_ERR_INVALID_ARG, "%s", "an output overlaps another argument");
+  gdn::NormArgs a{};
+  a.x = x;
+  a.y = y;
+  a.y_scale = y_scale;
+  a.rows = rows;
+  a.d = d;
+  a.in_dtype = in_dtype;
+  a.out_dtype = GDN_E4M3;
+  a.stream = static_cast<hipStream_t>(stream);
+  return hip_status(gdn::launch_quantize_rows(a), "gdn_quantize_rows launch");
+}
+
+GDN_API size_t gdn_add_rmsnorm_bwd_workspace_size(int64_t rows, int32_t d) {
+  if (rows < 0 || d <= 0 || d > gdn::kNormMaxD) return 0;
+  return gdn::add_rmsnorm_bwd_workspace_size(rows, d);
+}
+
+GDN_API int gdn_add_rmsnorm_bwd(const void *dy, const void *r, const void *dr,
+                                const float *norm_w, float rms_eps, void *dx, float *dnorm_w,
+                                int64_t rows, int32_t d, int32_t in_dtype, int32_t dy_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+  g_last_error[0] = '\0';
+  const int st = check_rows(rows, d);
+  if (st != GDN_OK) return st;
+  if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype))
+    return fail(GDN_ERR_UNSUPPORTED, "%s", "dtypes must be GDN_F32, GDN_BF16 or GDN_F16");
+  if (!(rms_eps >= 0.0f)) return fail(GDN_ERR_INVALID_ARG, "%s", "rms_eps must be >= 0");
+  if (rows > 0 && (!dy || !r || !dx))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "null input or output pointer");
+  if (misaligned(dy) || misaligned(r) || misaligned(dr) || misaligned(norm_w) || misaligned(dx) ||
+      misaligned(dnorm_w, 4))
+    return fail(GDN_ERR_MISALIGNED, "%s", "tensors and norm_w need 16-byte alignment, dnorm_w 4");
+  const size_t need = dnorm_w ? gdn::add_rmsnorm_bwd_workspace_size(rows, d) : 0;
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GDN_ERR_INVALID_ARG, "%s",
+                "workspace missing or smaller than gdn_add_rmsnorm_bwd_workspace_size");
+  if (need && misaligned(workspace, 256))
+    return fail(GDN_ERR_MISALIGNED, "%s", "workspace needs 256-byte alignment");
+  const size_t n = static_cast<size_t>(rows) * d, nw = static_cast<size_t>(d) * 4;
+  const size_t ni = n * esize(in_dtype);
+  const Span outs[3] = {{dx, ni}, {dnorm_w, nw}, {workspace, need}};
+  // dx may be dr itself: each element is read before it is written
+  const Span ins[4] = {{dy, n * esize(dy_dtype)}, {r, ni}, {dr == dx ? nullptr : dr, ni}, {norm_w, nw}};
+  if (!disjoint(ins, outs)) return fail(GDN_ERR_INVALID_ARG, "%s", "an output overlaps another argument");
+  gdn::NormBwdArgs a{};
+  a.dy = dy;
+  a.r = r;
+  a.dr = dr;
+  a.norm_w = norm_w;
+  a.eps = rms_eps;
+  a.dx = dx;
+  a.dnorm_w = dnorm_w;
+  a.part = dnorm_w ? static_cast<float *>(workspace) : nullptr;
+  a.rows = rows;
+  a.d = d;
+  a.in_dtype = in_dtype;
+  a.dy_dtype = dy_dtype;
+  a.stream = static_cast<hipStream_t>(stream);
+  return hip_status(gdn::launch_add_rmsnorm_bwd(a), "gdn_add_rmsnorm_bwd launch");
+}
+
+GDN_API size_t gdn_linear_workspace_size(int64_t M, int32_t N, int32_t K, int32_t in_dtype) {
+  if (!(dtype_ok(in_dtype) || in_dtype == GDN_E4M3) || !linear_sizes_ok(M, N, K, in_dtype)) return 0;
+  return gdn::linear_workspace_size(M, N, K, in_dtype);
+}
+
+GDN_API int gdn_linear(const void *x, const float *x_scale, const void *w, const float *w_scale,
+                       const float *bias, const void *residual, void *pre, void *y, int64_t M,
+                       int32_t N, int32_t K, int32_t act, int32_t in_dtype, int32_t out_dtype,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+  g_last_error[0] = '\0';
+  const bool e4m3 = in_dtype == GDN_E4M3;
+  if (!(dtype_ok(in_dtype) || e4m3) || !dtype_ok(out_dtype))
+    return fail(GDN_ERR_UNSUPPORTED, "%s",
+                "dtypes must be GDN_F32, GDN_BF16 or GDN_F16 (in_dtype also GDN_E4M3)");
+  if (!act_ok(act)) return fail(GDN_ERR_UNSUPPORTED, "%s", "unknown activation");
+  if (!linear_sizes_ok(M, N, K, in_dtype))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "M must be >= 0, N and K > 0, and rows at most 8 MiB");
+  if (M > 0 && (!x || !w || !y)) return fail(GDN_ERR_INVALID_ARG, "%s", "null input or output pointer");
+  if (M > 0 && (e4m3 != (x_scale != nullptr) || e4m3 != (w_scale != nullptr)))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "x_scale and w_scale go with GDN_E4M3 inputs");
+  if (misaligned(x) || misaligned(w) || misaligned(bias) || misaligned(w_scale) ||
+      misaligned(residual) || misaligned(pre) || misaligned(y) || misaligned(x_scale, 4))
+    return fail(GDN_ERR_MISALIGNED, "%s",
+                "tensors, bias and w_scale need 16-byte alignment, x_scale 4");
+  const size_t need = gdn::linear_workspace_size(M, N, K, in_dtype);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GDN_ERR_INVALID_ARG, "%s",
+                "workspace missing or smaller than gdn_linear_workspace_size");
+  if (need && misaligned(workspace, 256))
+    return fail(GDN_ERR_MISALIGNED, "%s", "workspace needs 256-byte alignment");
+  const size_t m = static_cast<size_t>(M), n4 = static_cast<size_t>(N) * 4;
+  const size_t ny = m * N * esize(out_dtype);
+  const Span outs[3] = {{pre, ny}, {y, ny}, {workspace, need}};
+  // y may be residual itself: each element is read before it is written
+  const Span ins[6] = {{x, m * K * esize_e4m3(in_dtype)},
+                       {w, static_cast<size_t>(N) * K * esize_e4m3(in_dtype)},
+                       {x_scale, m * 4},
+                       {w_scale, n4},
+                       {bias, n4},
+                       {residual == y ? nullptr : residual, ny}};
+  const Span res[1] = {{residual, ny}}, not_y[2] = {{pre, ny}, {workspace, need}};
+  if (!disjoint(ins, outs) || !disjoint(res, not_y))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "an output overlaps another argument");
+  gdn::LinearArgs a{};
+  a.x = x;
+  a.w = w;
+  a.x_scale = x_scale;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.residual = residual;
+  a.pre = pre;
+  a.y = y;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.in_dtype = in_dtype;
+  a.out_dtype = out_dtype;
+  a.ws = static_cast<char *>(workspace);
+  a.stream = static_cast<hipStream_t>(stream);
+  return hip_status(gdn::launch_linear(a), "gdn_linear launch");
+}
+
+GDN_API size_t gdn_linear_bwd_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act,
+                                             int32_t in_dtype, int32_t dy_dtype) {
+  if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype) || !act_ok(act) ||
+      !linear_sizes_ok(M, N, K, in_dtype) ||
+      M * static_cast<int64_t>(esize(in_dtype)) > kLinearMaxPitch)
+    return 0;
+  return gdn::linear_bwd_workspace_size(M, N, K, act, in_dtype, dy_dtype);
+}
+
+GDN_API int gdn_linear_bwd(const void *dy, const void *pre, const void *x, const void *w, void *dx,
+                           void *dw, float *dbias, int64_t M, int32_t N, int32_t K, int32_t act,
+                           int32_t in_dtype, int32_t dy_dtype, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+  g_last_error[0] = '\0';
+  if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype))
+    return fail(GDN_ERR_UNSUPPORTED, "%s", "dtypes must be GDN_F32, GDN_BF16 or GDN_F16");
+  if (!act_ok(act)) return fail(GDN_ERR_UNSUPPORTED, "%s", "unknown activation");
+  if (!linear_sizes_ok(M, N, K, in_dtype) ||
+      M * static_cast<int64_t>(esize(in_dtype)) > kLinearMaxPitch)
+    return fail(GDN_ERR_INVALID_ARG, "%s",
+                "M must be >= 0, N and K > 0, and rows and columns at most 8 MiB");
+  if (M > 0 && !dy) return fail(GDN_ERR_INVALID_ARG, "%s", "dy is required");
+  if (M > 0 && act != GDN_ACT_NONE && !pre)
+    return fail(GDN_ERR_INVALID_ARG, "%s", "an activation needs pre");
+  if (M > 0 && ((dx && !w) || (dw && !x)))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "dx needs w, dw needs x");
+  if (misaligned(dy) || misaligned(pre) || misaligned(x) || misaligned(w) || misaligned(dx) ||
+      misaligned(dw) || misaligned(dbias, 4))
+    return fail(GDN_ERR_MISALIGNED, "%s", "tensors need 16-byte alignment, dbias 4");
+  const size_t need = gdn::linear_bwd_workspace_size(M, N, K, act, in_dtype, dy_dtype);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GDN_ERR_INVALID_ARG, "%s",
+                "workspace missing or smaller than gdn_linear_bwd_workspace_size");
+  if (need && misaligned(workspace, 256))
+    return fail(GDN_ERR_MISALIGNED, "%s", "workspace needs 256-byte alignment");
+  const size_t m = static_cast<size_t>(M), n = static_cast<size_t>(N), k = static_cast<size_t>(K);
+  const size_t e = esize(in_dtype), ng = m * n * esize(dy_dtype);
+  const Span outs[4] = {{dx, m * k * e}, {dw, n * k * e}, {dbias, n * 4}, {workspace, need}};
+  const Span ins[4] = {{dy, ng}, {pre, ng}, {x, m * k * e}, {w, n * k * e}};
+  if (!disjoint(ins, outs)) return fail(GDN_ERR_INVALID_ARG, "%s", "an output overlaps another argument");
+  gdn::LinearBwdArgs a{};
+  a.dy = dy;
+  a.pre = pre;
+  a.x = x;
+  a.w = w;
+  a.dx = dx;
+  a.dw = dw;
+  a.dbias = dbias;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.act = act;
+  a.in_dtype = in_dtype;
+  a.dy_dtype = dy_dtype;
+  a.ws = static_cast<char *>(workspace);
+  a.stream = static_cast<hipStream_t>(stream);
+  return hip_status(gdn::launch_linear_bwd(a), "gdn_linear_bwd launch");
+}
+
+}  // extern "C"

@@ -16,6 +16,10 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // bf16 is carried as its 16 raw bits.
 typedef uint16_t bf16_t;
+// OCP e4m3 (no infinities, largest value 448) as its 8 raw bits.
+struct e4m3_t {
+  uint8_t bits;
+};
 
 __device__ __forceinline__ float bf16_to_f32(bf16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);

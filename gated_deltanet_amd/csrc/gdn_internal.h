@@ -154,6 +154,78 @@ struct ConvStateArgs {
 
 hipError_t launch_conv_state(const ConvStateArgs &a);
 
+constexpr int kE4m3 = 3;           // dtype code of e4m3, beside 0 f32, 1 bf16, 2 f16
+constexpr int kNormMaxD = 32768;   // widest row of the norm and the quantiser
+
+// Residual addition + RMSNorm; the row quantiser uses x, y, y_scale, rows, d,
+// in_dtype and stream only.
+struct NormArgs {
+  const void *x, *residual;  // [rows, d] in_dtype; residual may be null
+  const float *norm_w;       // [d] or null
+  float eps;
+  void *r;                   // x + residual in in_dtype, or null
+  void *y;                   // [rows, d] out_dtype
+  float *y_scale;            // [rows], e4m3 outputs only
+  int64_t rows;
+  int d;
+  int in_dtype, out_dtype;
+  hipStream_t stream;
+};
+
+struct NormBwdArgs {
+  const void *dy;            // [rows, d] dy_dtype
+  const void *r, *dr;        // [rows, d] in_dtype; dr may be null
+  const float *norm_w;       // [d] or null
+  float eps;
+  void *dx;                  // [rows, d] in_dtype
+  float *dnorm_w;            // [d] or null
+  float *part;               // workspace, null without dnorm_w
+  int64_t rows;
+  int d;
+  int in_dtype, dy_dtype;
+  hipStream_t stream;
+};
+
+// y = act(x w^T + bias) + residual
+struct LinearArgs {
+  const void *x, *w;                // [M, K], [N, K] in in_dtype
+  const float *x_scale, *w_scale;   // [M], [N], e4m3 inputs only
+  const float *bias;                // [N] or null
+  const void *residual;             // [M, N] out_dtype or null
+  void *pre;                        // x w^T + bias, [M, N] out_dtype, or null
+  void *y;                          // [M, N] out_dtype
+  int64_t M;
+  int N, K;
+  int act;                          // 0 none, 1 silu, 2 gelu, 3 sigmoid
+  int in_dtype, out_dtype;
+  char *ws;                         // workspace, 256-byte aligned
+  hipStream_t stream;
+};
+
+struct LinearBwdArgs {
+  const void *dy, *pre;             // [M, N] dy_dtype; pre null without an activation
+  const void *x, *w;                // [M, K], [N, K] in in_dtype
+  void *dx, *dw;                    // [M, K], [N, K] in in_dtype, or null
+  float *dbias;                     // [N] or null
+  int64_t M;
+  int N, K;
+  int act;
+  int in_dtype, dy_dtype;
+  char *ws;
+  hipStream_t stream;
+};
+
+hipError_t launch_add_rmsnorm(const NormArgs &a);
+hipError_t launch_quantize_rows(const NormArgs &a);
+size_t add_rmsnorm_bwd_workspace_size(int64_t rows, int d);
+hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs &a);
+// out[c] = sum of part[p][c] over p < P, in a fixed order
+hipError_t launch_colsum(const float *part, int P, int d, float *out, hipStream_t stream);
+size_t linear_workspace_size(int64_t M, int N, int K, int in_dtype);
+hipError_t launch_linear(const LinearArgs &a);
+size_t linear_bwd_workspace_size(int64_t M, int N, int K, int act, int in_dtype, int dy_dtype);
+hipError_t launch_linear_bwd(const LinearBwdArgs &a);
+
 // Bookkeeping of the segment-parallel prefill (segment.hip): segment bounds
 // (N x (P + 1)), initial states of the zero-start runs (N x (P - 1) states,
 // the first of each sequence the caller's S0), n_ident identity matrices and

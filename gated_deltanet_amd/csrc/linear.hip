@@ -1,0 +1,650 @@
+// Matrix product with bias, activation and residual in its epilogue, and its
+// backward pass (gfx950):
+//
+//     u = x w^T + bias        y = act(u) + residual
+//     du = dy act'(u)         dx = du w     dw = du^T x     dbias = sum over rows of du
+//
+// Every product is the same kernel: C[m][n] = sum_r P[m][r] Q[n][r], both
+// operands with the reduction index r contiguous, rows a whole number of
+// 16-byte vectors apart. Operands that are not laid out so (odd widths, the
+// transposes that the backward reduces over) are first copied into the
+// workspace, padded with zeros.
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 128;  // output tile of a workgroup
+constexpr int kStep = 128;  // bytes of the reduction axis per step
+
+// ---------------------------------------------------------------------------
+// epilogue
+
+struct Epilogue {
+  const float *x_scale, *w_scale, *bias;  // [M], [N], [N] or null
+  const void *residual;                   // [M, N] out_dtype or null
+  void *pre, *y;                          // [M, N] out_dtype; pre may be null
+  int64_t M;
+  int N;
+  int act, out_dtype;
+};
+
+// 1 / (1 + exp(-u)), see sigmoid() for its ends
+__device__ __forceinline__ float act_fwd(float u, int act) {
+  switch (act) {
+    case 1: return u * sigmoid(u);
+    case 2: return 0.5f * u * (1.0f + erff(u * 0.70710678f));
+    case 3: return sigmoid(u);
+    default: return u;
+  }
+}
+
+__device__ __forceinline__ float act_slope(float u, int act) {
+  switch (act) {
+    case 1: {
+      const float p = sigmoid(u);
+      return p * (1.0f + u * (1.0f - p));
+    }
+    case 2:  // the normal distribution's integral + u times its density
+      return 0.5f * (1.0f + erff(u * 0.70710678f)) +
+             u * 0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * u * u);
+    case 3: {
+      const float p = sigmoid(u);
+      return p * (1.0f - p);
+    }
+    default: return 1.0f;
+  }
+}
+
+template <typename T>
+struct Vec4;
+template <>
+struct Vec4<float> {
+  __device__ static __forceinline__ f32x4 load(const float *p) {
+    return *reinterpret_cast<const f32x4 *>(p);
+  }
+  __device__ static __forceinline__ void store(float *p, f32x4 v) {
+    *reinterpret_cast<f32x4 *>(p) = v;
+  }
+};
+template <>
+struct Vec4<_Float16> {
+  __device__ static __forceinline__ f32x4 load(const _Float16 *p) {
+    return __builtin_convertvector(*reinterpret_cast<const f16x4 *>(p), f32x4);
+  }
+  __device__ static __forceinline__ void store(_Float16 *p, f32x4 v) {
+    *reinterpret_cast<f16x4 *>(p) = __builtin_convertvector(v, f16x4);
+  }
+};
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+template <>
+struct Vec4<bf16_t> {
+  __device__ static __forceinline__ f32x4 load(const bf16_t *p) {
+    return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(p), f32x4);
+  }
+  __device__ static __forceinline__ void store(bf16_t *p, f32x4 v) {
+    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(v, bf16x4);
+  }
+};
+
+// four consecutive elements of a row; `whole`: all four exist and are aligned,
+// else the first cnt of them do
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T *p, bool whole, int cnt) {
+  if (whole) return Vec4<T>::load(p);
+  f32x4 v = zero4();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < cnt) v[i] = io<T>::to_f32(p[i]);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store4(T *p, f32x4 v, bool whole, int cnt) {
+  if (whole) {
+    Vec4<T>::store(p, v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < cnt) p[i] = io<T>::from_f32(v[i]);
+}
+
+template <typename TO>
+__device__ __forceinline__ void epilogue4_as(const Epilogue &e, int64_t m, int n, f32x4 v) {
+  const bool whole = e.N % 4 == 0;
+  const int cnt = e.N - n;
+  const size_t at = static_cast<size_t>(m) * e.N + n;
+  if (e.w_scale) {
+    const float xs = e.x_scale[m];
+    const f32x4 ws = load4(e.w_scale + n, whole, cnt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= xs * ws[i];
+  }
+  if (e.bias) {
+    const f32x4 b = load4(e.bias + n, whole, cnt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += b[i];
+  }
+  if (e.pre) store4(static_cast<TO *>(e.pre) + at, v, whole, cnt);
+  if (e.act) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = act_fwd(v[i], e.act);
+  }
+  if (e.residual) {
+    const f32x4 r = load4(static_cast<const TO *>(e.residual) + at, whole, cnt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += r[i];
+  }
+  store4(static_cast<TO *>(e.y) + at, v, whole, cnt);
+}
+
+// u[m][n .. n + 3] (n a multiple of 4, m < M, n < N) through the epilogue
+__device__ __forceinline__ void epilogue4(const Epilogue &e, int64_t m, int n, f32x4 v) {
+  if (e.out_dtype == 1) epilogue4_as<bf16_t>(e, m, n, v);
+  else if (e.out_dtype == 2) epilogue4_as<_Float16>(e, m, n, v);
+  else epilogue4_as<float>(e, m, n, v);
+}
+
+// ---------------------------------------------------------------------------
+// tile kernel
+
+// eight e4m3 values as fp16
+__device__ __forceinline__ f16x8 widen_e4m3(uint32_t lo, uint32_t hi) {
+  struct Quad {
+    f16x2 v[4];
+  } q;
+  q.v[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+  q.v[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+  q.v[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+  q.v[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+  return __builtin_bit_cast(f16x8, q);
+}
+
+// acc += A B over the 32 bytes of the reduction axis that the lane holds of
+// one operand row: two 16-byte vectors. The lanes lg = 0..3 of a row hold
+// bytes 16 lg and 64 + 16 lg of the 128-byte step; the matrix cores pair the
+// operands slot by slot, so any assignment of reduction indices to slots that
+// both operands share gives the product.
+//
+// The 8-bit matrix instructions take the products of a lane's 8 consecutive
+// bytes together, each cut off 13 bits below the largest's exponent (observed
+// on the card; the 16x16x32 and 16x16x128 forms alike): relative errors of
+// about 1.5e-5 of the result, well under the rounding of a 16-bit output, but
+// not of an fp32 one. EXACT widens e4m3 to fp16 (which holds every e4m3
+// value) and uses the 16-bit instructions, whose sums are good to fp32.
+template <typename T, bool EXACT>
+__device__ __forceinline__ f32x4 mma_step(const u32x4 (&a)[2], const u32x4 (&b)[2], f32x4 acc) {
+  if constexpr (__is_same(T, bf16_t)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[h]),
+                                                    __builtin_bit_cast(bf16x8, b[h]), acc, 0, 0, 0);
+  } else if constexpr (__is_same(T, _Float16)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a[h]),
+                                                   __builtin_bit_cast(f16x8, b[h]), acc, 0, 0, 0);
+  } else if constexpr (__is_same(T, float)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[h][i]),
+                                                   __uint_as_float(b[h][i]), acc, 0, 0, 0);
+  } else if constexpr (EXACT) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_e4m3(a[h][2 * q], a[h][2 * q + 1]),
+                                                     widen_e4m3(b[h][2 * q], b[h][2 * q + 1]), acc,
+                                                     0, 0, 0);
+  } else {
+    typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+    struct Pair {
+      u32x4 v[2];
+    };
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        __builtin_bit_cast(i32x8, Pair{{a[0], a[1]}}), __builtin_bit_cast(i32x8, Pair{{b[0], b[1]}}),
+        acc, 0, 0, 0, 0, 0, 0);  // e4m3 by e4m3, no block scales
+  }
+  return acc;
+}
+
+struct GemmArgs {
+  const char *p, *q;         // operands: [M] rows, [N] rows
+  int64_t ldp, ldq;          // bytes between rows, multiples of 16
+  int64_t M;
+  int N;
+  int rbytes;                // bytes of the reduction axis, a multiple of 16
+  int steps;                 // kStep-byte steps per split
+  float *part;               // null: epilogue; else [splits][M][ldpart] sums
+  int64_t ldpart;
+  int tiles_n;
+  Epilogue e;
+};
+
+// One kTile x kTile tile of C (times one split of the reduction) per workgroup
+// of four waves, each 64 x 64 of it in 16 x 16 accumulators. A stage holds
+// 128 bytes of the reduction axis of every operand row, loaded straight to
+// LDS; the next stage is in flight while one is multiplied.
+template <typename T, bool EXACT>
+__global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
+  constexpr int STAGE = 2 * kTile * kStep;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int lc = lane % 16, lg = lane / 16;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x / g.tiles_n) * kTile;
+  const int n0 = static_cast<int>(blockIdx.x % g.tiles_n) * kTile;
+  const int wm = (wave / 2) * 64, wn = (wave % 2) * 64;
+
+  // rows past the operand's end lie past the resource's end and read as zeros
+  const int64_t mrows = g.M - m0 < kTile ? g.M - m0 : kTile;
+  const int nrows = g.N - n0 < kTile ? g.N - n0 : kTile;
+  const i32x4 rp = buffer_rsrc(g.p + m0 * g.ldp, static_cast<uint32_t>(mrows * g.ldp));
+  const i32x4 rq = buffer_rsrc(g.q + n0 * g.ldq, static_cast<uint32_t>(nrows * g.ldq));
+
+  // A load instruction covers 8 rows of 128 bytes; lane L lands at byte 16 L
+  // of its 1 KiB, row L / 8, vector L % 8. It fetches vector (L % 8) ^ (row % 8)
+  // of its row, so that the fragment reads below touch all banks evenly.
+  const int row = lane / 8;
+  const int vecoff = ((lane % 8) ^ row) * 16;
+  const int s0 = blockIdx.y * g.steps;
+  const int total = (g.rbytes + kStep - 1) / kStep;
+  const int s1 = s0 + g.steps < total ? s0 + g.steps : total;
+  auto issue = [&](int s, int buf) {
+    const int r = s * kStep + vecoff;
+    const bool in = r < g.rbytes;
+    const uint32_t base = lds_addr(smem) + buf * STAGE;
+#pragma unroll
+    for (int i = 0; i < kTile / 32; ++i) {
+      const int blk = wave + 4 * i;
+      const uint32_t op = static_cast<uint32_t>((blk * 8 + row) * g.ldp) + r;
+      const uint32_t oq = static_cast<uint32_t>((blk * 8 + row) * g.ldq) + r;
+      dma16(rp, in ? op : 0x80000000u, base + blk * 1024);
+      dma16(rq, in ? oq : 0x80000000u, base + kTile * kStep + blk * 1024);
+    }
+  };
+
+  f32x4 acc[4][4];  // [n tile][m tile]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = zero4();
+
+  if (s0 < s1) issue(s0, 0);
+  for (int s = s0; s < s1; ++s) {
+    const int buf = (s - s0) & 1;
+    wait_vmcnt<0>();
+    wg_barrier();
+    if (s + 1 < s1) issue(s + 1, buf ^ 1);
+    const char *base = smem + buf * STAGE;
+    const int o0 = lc * 128 + ((lg ^ (lc & 7)) * 16);
+    u32x4 a[4][2], b[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int o = o0 ^ (64 * h);
+        a[i][h] = *reinterpret_cast<const u32x4 *>(base + kTile * kStep + (wn + 16 * i) * 128 + o);
+        b[i][h] = *reinterpret_cast<const u32x4 *>(base + (wm + 16 * i) * 128 + o);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mma_step<T, EXACT>(a[i], b[j], acc[i][j]);
+  }
+
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t m = m0 + wm + 16 * j + lc;
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + wn + 16 * i + 4 * lg;
+      if (n >= g.N) continue;
+      if (g.part)
+        *reinterpret_cast<f32x4 *>(g.part + (static_cast<size_t>(blockIdx.y) * g.M + m) * g.ldpart +
+                                   n) = acc[i][j];
+      else
+        epilogue4(g.e, m, n, acc[i][j]);
+    }
+  }
+}
+
+// partial sums of the splits, added in order, through the epilogue
+__global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ part, int splits,
+                                                   int64_t ldpart, const Epilogue e) {
+  const int64_t quads = ldpart / 4;
+  const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (q >= e.M * quads) return;
+  const int64_t m = q / quads;
+  const int n = static_cast<int>(q % quads) * 4;
+  f32x4 v = *reinterpret_cast<const f32x4 *>(part + m * ldpart + n);
+  for (int s = 1; s < splits; ++s)
+    v += *reinterpret_cast<const f32x4 *>(part + (static_cast<size_t>(s) * e.M + m) * ldpart + n);
+  epilogue4(e, m, n, v);
+}
+
+// ---------------------------------------------------------------------------
+// operand layout
+
+// dst[r][0 .. pitch) = src[r][0 .. cols) and zeros (E: raw bits of an element)
+template <typename E>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const E *__restrict__ src, int64_t rows,
+                                                       int cols, E *__restrict__ dst, int pitch) {
+  const int64_t total = rows * pitch;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / pitch;
+    const int c = static_cast<int>(i % pitch);
+    dst[i] = c < cols ? src[r * cols + c] : E(0);
+  }
+}
+
+// dst[c][0 .. pitch) = src[0 .. rows)[c] and zeros, by 64 x 64 tiles
+template <typename E>
+__global__ __launch_bounds__(256) void transpose_kernel(const E *__restrict__ src, int64_t rows,
+                                                        int cols, int64_t ld, E *__restrict__ dst,
+                                                        int64_t pitch) {
+  __shared__ E s[64][65];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64;
+  const int c0 = blockIdx.y * 64;
+  const int lo = threadIdx.x % 64, hi = threadIdx.x / 64;
+  for (int i = hi; i < 64; i += 4)
+    s[i][lo] = r0 + i < rows && c0 + lo < cols ? src[(r0 + i) * ld + c0 + lo] : E(0);
+  __syncthreads();
+  for (int i = hi; i < 64; i += 4)
+    if (c0 + i < cols && r0 + lo < pitch) dst[(c0 + i) * pitch + r0 + lo] = s[lo][i];
+}
+
+// du[m][0 .. pitch) = dy act'(pre), zeros from N on (du may be null), and the
+// column sums of du over each run of `run` rows (part may be null). A
+// workgroup owns 64 columns of one run.
+template <typename TG, typename T>
+__global__ __launch_bounds__(256) void du_kernel(const TG *__restrict__ dy,
+                                                 const TG *__restrict__ pre, int64_t M, int N,
+                                                 int act, T *__restrict__ du, int pitch, int run,
+                                                 float *__restrict__ part) {
+  __shared__ float s[4][64];
+  const int lo = threadIdx.x % 64, hi = threadIdx.x / 64;
+  const int n = blockIdx.x * 64 + lo;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * run;
+  const int64_t m1 = m0 + run < M ? m0 + run : M;
+  float sum = 0.0f;
+  for (int64_t m = m0 + hi; m < m1; m += 4) {
+    float v = 0.0f;
+    if (n < N) {
+      v = io<TG>::to_f32(dy[m * N + n]);
+      if (act) v *= act_slope(io<TG>::to_f32(pre[m * N + n]), act);
+    }
+    sum += v;
+    if (du && n < pitch) du[m * pitch + n] = io<T>::from_f32(v);
+  }
+  if (!part) return;
+  s[hi][lo] = sum;
+  __syncthreads();
+  if (hi == 0 && n < N)
+    part[static_cast<size_t>(blockIdx.y) * N + n] = ((s[0][lo] + s[1][lo]) + s[2][lo]) + s[3][lo];
+}
+
+// ---------------------------------------------------------------------------
+// plans
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+int esize(int t) { return t == 0 ? 4 : t == kE4m3 ? 1 : 2; }
+int64_t round16(int64_t x) { return (x + 15) / 16 * 16; }
+
+template <typename F>
+hipError_t with_type(int code, F &&f) {
+  switch (code) {
+    case 1: return f(bf16_t{});
+    case 2: return f(_Float16{});
+    default: return f(float{});
+  }
+}
+
+// One product: how the reduction is split and what that needs.
+struct GemmPlan {
+  int64_t tiles_m;
+  int tiles_n;
+  int splits, steps;
+  int64_t ldpart;
+  size_t part_bytes;
+};
+
+// Few output tiles leave CUs idle: the reduction is then split until about 256
+// workgroups run, each keeping at least four steps.
+GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes) {
+  GemmPlan p;
+  p.tiles_m = (M + kTile - 1) / kTile;
+  p.tiles_n = (N + kTile - 1) / kTile;
+  const int total = static_cast<int>((rbytes + kStep - 1) / kStep);
+  const int64_t tiles = p.tiles_m * p.tiles_n;
+  int64_t want = tiles > 0 ? 256 / tiles : 1;
+  if (want > total / 4) want = total / 4;
+  if (want < 1) want = 1;
+  p.steps = static_cast<int>((total + want - 1) / want);
+  if (p.steps < 1) p.steps = 1;
+  p.splits = total > 0 ? (total + p.steps - 1) / p.steps : 1;
+  p.ldpart = (N + 3) / 4 * 4;
+  p.part_bytes = p.splits > 1 ? align256(static_cast<size_t>(p.splits) * M * p.ldpart * 4) : 0;
+  return p;
+}
+
+hipError_t run_gemm(const void *P, int64_t ldp, const void *Q, int64_t ldq, int64_t M, int N,
+                    int64_t rbytes, int dtype, const Epilogue &e, char *part, hipStream_t stream) {
+  if (M == 0) return hipSuccess;
+  const GemmPlan p = plan_gemm(M, N, rbytes);
+  GemmArgs g;
+  g.p = static_cast<const char *>(P);
+  g.q = static_cast<const char *>(Q);
+  g.ldp = ldp;
+  g.ldq = ldq;
+  g.M = M;
+  g.N = N;
+  g.rbytes = static_cast<int>(rbytes);
+  g.steps = p.steps;
+  g.part = p.splits > 1 ? reinterpret_cast<float *>(part) : nullptr;
+  g.ldpart = p.ldpart;
+  g.tiles_n = p.tiles_n;
+  g.e = e;
+  const dim3 grid(static_cast<unsigned>(p.tiles_m * p.tiles_n), p.splits);
+  if (dtype == kE4m3 && e.out_dtype == 0)
+    hipLaunchKernelGGL((gemm_kernel<e4m3_t, true>), grid, dim3(256), 0, stream, g);
+  else if (dtype == kE4m3)
+    hipLaunchKernelGGL((gemm_kernel<e4m3_t, false>), grid, dim3(256), 0, stream, g);
+  else if (dtype == 1)
+    hipLaunchKernelGGL((gemm_kernel<bf16_t, true>), grid, dim3(256), 0, stream, g);
+  else if (dtype == 2)
+    hipLaunchKernelGGL((gemm_kernel<_Float16, true>), grid, dim3(256), 0, stream, g);
+  else
+    hipLaunchKernelGGL((gemm_kernel<float, true>), grid, dim3(256), 0, stream, g);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || !g.part) return err;
+  const int64_t quads = M * (p.ldpart / 4);
+  hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0,
+                     stream, g.part, p.splits, p.ldpart, e);
+  return hipGetLastError();
+}
+
+template <typename F>
+void by_size(int es, F &&f) {
+  if (es == 4) f(uint32_t{});
+  else if (es == 2) f(uint16_t{});
+  else f(uint8_t{});
+}
+
+hipError_t pad_rows(const void *src, int64_t rows, int cols, void *dst, int pitch, int es,
+                    hipStream_t stream) {
+  const int64_t blocks = (rows * pitch + 1023) / 1024;
+  by_size(es, [&](auto e) {
+    using E = decltype(e);
+    hipLaunchKernelGGL(pad_rows_kernel<E>, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)),
+                       dim3(256), 0, stream, static_cast<const E *>(src), rows, cols,
+                       static_cast<E *>(dst), pitch);
+  });
+  return hipGetLastError();
+}
+
+hipError_t transpose(const void *src, int64_t rows, int cols, int64_t ld, void *dst, int64_t pitch,
+                     int es, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((pitch + 63) / 64), (cols + 63) / 64);
+  by_size(es, [&](auto e) {
+    using E = decltype(e);
+    hipLaunchKernelGGL(transpose_kernel<E>, grid, dim3(256), 0, stream,
+                       static_cast<const E *>(src), rows, cols, ld, static_cast<E *>(dst), pitch);
+  });
+  return hipGetLastError();
+}
+
+// forward workspace: padded copies of x and w where K is no whole vector,
+// then the partial sums
+struct FwdLayout {
+  int64_t pitch;  // elements between rows of the operands in use
+  bool pad;
+  size_t x, w, part, total;
+};
+FwdLayout fwd_layout(int64_t M, int N, int K, int dtype) {
+  const int es = esize(dtype);
+  FwdLayout L;
+  const int64_t rb = round16(static_cast<int64_t>(K) * es);
+  L.pitch = rb / es;
+  L.pad = L.pitch != K;
+  size_t off = 0;
+  L.x = off;
+  if (L.pad) off += align256(static_cast<size_t>(M) * rb);
+  L.w = off;
+  if (L.pad) off += align256(static_cast<size_t>(N) * rb);
+  L.part = off;
+  off += plan_gemm(M, N, rb).part_bytes;
+  L.total = off;
+  return L;
+}
+
+constexpr int kDuRuns = 256;  // most runs of rows whose column sums are kept
+int du_run(int64_t M) {
+  const int64_t r = (M + kDuRuns - 1) / kDuRuns;
+  return static_cast<int>(r < 64 ? 64 : r);
+}
+
+// backward workspace: du (when it is not dy itself), the transposes of w, du
+// and x, partial sums of dbias, partial sums of one product at a time
+struct BwdLayoutL {
+  bool own_du;
+  int64_t pn, pm;  // pitches of du and w^T (over N), of du^T and x^T (over M)
+  size_t du, wt, dut, xt, db, part, total;
+};
+BwdLayoutL bwd_layout(int64_t M, int N, int K, int act, int in_dtype, int dy_dtype) {
+  const int es = esize(in_dtype);
+  BwdLayoutL L;
+  const int64_t rn = round16(static_cast<int64_t>(N) * es), rm = round16(M * es);
+  L.pn = rn / es;
+  L.pm = rm / es;
+  L.own_du = act != 0 || dy_dtype != in_dtype || L.pn != N;
+  size_t off = 0;
+  L.du = off;
+  if (L.own_du) off += align256(static_cast<size_t>(M) * rn);
+  L.wt = off;
+  off += align256(static_cast<size_t>(K) * rn);
+  L.dut = off;
+  off += align256(static_cast<size_t>(N) * rm);
+  L.xt = off;
+  off += align256(static_cast<size_t>(K) * rm);
+  L.db = off;
+  off += align256(static_cast<size_t>((M + du_run(M) - 1) / du_run(M)) * N * 4);
+  L.part = off;
+  const size_t p1 = plan_gemm(M, K, rn).part_bytes, p2 = plan_gemm(N, K, rm).part_bytes;
+  off += p1 > p2 ? p1 : p2;
+  L.total = off;
+  return L;
+}
+
+}  // namespace
+
+size_t linear_workspace_size(int64_t M, int N, int K, int in_dtype) {
+  return fwd_layout(M, N, K, in_dtype).total;
+}
+
+hipError_t launch_linear(const LinearArgs &a) {
+  if (a.M == 0) return hipSuccess;
+  const FwdLayout L = fwd_layout(a.M, a.N, a.K, a.in_dtype);
+  const int es = esize(a.in_dtype);
+  const void *x = a.x, *w = a.w;
+  if (L.pad) {
+    hipError_t err = pad_rows(a.x, a.M, a.K, a.ws + L.x, static_cast<int>(L.pitch), es, a.stream);
+    if (err != hipSuccess) return err;
+    err = pad_rows(a.w, a.N, a.K, a.ws + L.w, static_cast<int>(L.pitch), es, a.stream);
+    if (err != hipSuccess) return err;
+    x = a.ws + L.x;
+    w = a.ws + L.w;
+  }
+  const Epilogue e{a.x_scale, a.w_scale, a.bias, a.residual, a.pre, a.y, a.M, a.N, a.act,
+                   a.out_dtype};
+  return run_gemm(x, L.pitch * es, w, L.pitch * es, a.M, a.N, L.pitch * es, a.in_dtype, e,
+                  a.ws + L.part, a.stream);
+}
+
+size_t linear_bwd_workspace_size(int64_t M, int N, int K, int act, int in_dtype, int dy_dtype) {
+  return bwd_layout(M, N, K, act, in_dtype, dy_dtype).total;
+}
+
+hipError_t launch_linear_bwd(const LinearBwdArgs &a) {
+  const BwdLayoutL L = bwd_layout(a.M, a.N, a.K, a.act, a.in_dtype, a.dy_dtype);
+  const int es = esize(a.in_dtype);
+  const int run = du_run(a.M);
+  const int runs = static_cast<int>((a.M + run - 1) / run);
+  const void *du = L.own_du ? a.ws + L.du : a.dy;
+  float *db = reinterpret_cast<float *>(a.ws + L.db);
+  hipError_t err = hipSuccess;
+  if (a.M > 0 && (L.own_du || a.dbias)) {
+    err = with_type(a.in_dtype, [&](auto t) {
+      return with_type(a.dy_dtype, [&](auto tg) {
+        using T = decltype(t);
+        using TG = decltype(tg);
+        hipLaunchKernelGGL((du_kernel<TG, T>), dim3(static_cast<unsigned>((L.pn + 63) / 64), runs),
+                           dim3(256), 0, a.stream, static_cast<const TG *>(a.dy),
+                           static_cast<const TG *>(a.pre), a.M, a.N, a.act,
+                           L.own_du ? reinterpret_cast<T *>(a.ws + L.du) : nullptr,
+                           static_cast<int>(L.pn), run, a.dbias ? db : nullptr);
+        return hipGetLastError();
+      });
+    });
+    if (err != hipSuccess) return err;
+  }
+  if (a.dbias) {
+    err = launch_colsum(db, runs, a.N, a.dbias, a.stream);
+    if (err != hipSuccess) return err;
+  }
+  Epilogue e{};
+  e.N = a.K;
+  e.out_dtype = a.in_dtype;
+  if (a.dx && a.M > 0) {
+    err = transpose(a.w, a.N, a.K, a.K, a.ws + L.wt, L.pn, es, a.stream);
+    if (err != hipSuccess) return err;
+    e.M = a.M;
+    e.y = a.dx;
+    err = run_gemm(du, L.pn * es, a.ws + L.wt, L.pn * es, a.M, a.K, L.pn * es, a.in_dtype, e,
+                   a.ws + L.part, a.stream);
+    if (err != hipSuccess) return err;
+  }
+  if (a.dw) {
+    if (a.M > 0) {
+      err = transpose(du, a.M, a.N, L.pn, a.ws + L.dut, L.pm, es, a.stream);
+      if (err != hipSuccess) return err;
+      err = transpose(a.x, a.M, a.K, a.K, a.ws + L.xt, L.pm, es, a.stream);
+      if (err != hipSuccess) return err;
+    }
+    e.M = a.N;
+    e.y = a.dw;
+    err = run_gemm(a.ws + L.dut, L.pm * es, a.ws + L.xt, L.pm * es, a.N, a.K, L.pm * es,
+                   a.in_dtype, e, a.ws + L.part, a.stream);
+  }
+  return err;
+}
+
+}  // namespace gdn

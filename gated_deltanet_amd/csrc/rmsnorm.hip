@@ -1,0 +1,368 @@
+// Residual addition + RMSNorm, its backward pass and the row quantiser
+// (gfx950).
+//
+//     r = x + residual                    y = r / sqrt(mean(r^2) + eps) * (1 + w)
+//     e4m3 output: scale = max(max |y|, 1e-30) / 448 per row, q = y / scale
+// and, for L = <dy, y> + <dr, r> with g = dy (1 + w), rs = 1 / sqrt(mean(r^2) + eps),
+//     dL/dr = dr + rs (g - r rs^2 mean(g r)),   dL/dw = sum over rows of dy r rs
+// (dL/dr is the gradient of x and of the residual alike). The weight is the
+// zero-centred one of the output gate (gain 1 + w).
+//
+// All three are HBM streams of a few flops per byte. A row is held in the
+// registers of the NT threads that own it (up to kChunks groups of 8 elements
+// each), so every input is read once and every output written once; sums,
+// maxima and the normalised values stay in fp32 and are rounded once, when
+// they are stored.
+#include <type_traits>
+
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kChunks = 4;          // 8-element groups per thread
+constexpr float kE4m3Max = 448.0f;  // largest finite e4m3 value
+// Rows whose absolute maximum is below this (zero rows among them) take it as
+// their maximum: the scale stays a normal number and its reciprocal finite.
+constexpr float kTinyMax = 1e-30f;
+
+// Elements e0 .. e0 + 7 of a row of d, zeros past the end. `vec`: d is a
+// multiple of 8, so that every group is whole and 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int e0, int d, bool vec, float *o) {
+  if (vec) {
+    if (e0 < d) {
+      Vec8<T>::load(row + e0, o);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = e0 + i < d ? io<T>::to_f32(row[e0 + i]) : 0.0f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *row, int e0, int d, bool vec, const float *v) {
+  if (vec) {
+    if (e0 < d) Vec8<T>::store(row + e0, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e0 + i < d) row[e0 + i] = io<T>::from_f32(v[i]);
+  }
+}
+
+// e4m3 bytes of eight values already divided by the row's scale. |v| is at
+// most 448 (1 + 2^-22), which rounds to 448: the conversion cannot overflow.
+__device__ __forceinline__ u32x2 to_e4m3(const float *v) {
+  u32x2 r;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
+    r[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], p, true);
+  }
+  return r;
+}
+
+template <>
+__device__ __forceinline__ void store8<e4m3_t>(e4m3_t *row, int e0, int d, bool vec,
+                                               const float *v) {
+  const u32x2 q = to_e4m3(v);
+  if (vec) {
+    if (e0 < d) *reinterpret_cast<u32x2 *>(row + e0) = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e0 + i < d) row[e0 + i].bits = static_cast<uint8_t>(q[i / 4] >> (8 * (i % 4)));
+  }
+}
+
+// the larger of two values, NaN if either is (a NaN in a row reaches its scale)
+__device__ __forceinline__ float max_nan(float m, float v) { return (v > m || v != v) ? v : m; }
+
+struct Add {
+  __device__ static __forceinline__ float of(float a, float b) { return a + b; }
+};
+struct Max {
+  __device__ static __forceinline__ float of(float a, float b) { return max_nan(a, b); }
+};
+
+// All-reduce of K values over the NT threads of a row, in a fixed order. Rows
+// wider than a wave are joined in `part` (NT / 64 entries per value).
+template <int NT, int K, typename Op>
+__device__ __forceinline__ void row_reduce(float (&v)[K], float *part) {
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int s = 1; s < (NT < 64 ? NT : 64); s *= 2) v[k] = Op::of(v[k], __shfl_xor(v[k], s));
+  if constexpr (NT > 64) {
+    constexpr int W = NT / 64;
+    const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    __syncthreads();  // an earlier reduction's readers are done with `part`
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) part[k * W + wave] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k] = part[k * W];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v[k] = Op::of(v[k], part[k * W + w]);
+    }
+  }
+}
+
+// NT threads own a row; a workgroup of max(NT, 256) threads owns one or more.
+// NORM false: y = x (the row quantiser).
+template <typename TI, typename TO, int NT, bool NORM>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(const NormArgs a) {
+  constexpr int RPB = NT < 256 ? 256 / NT : 1;
+  __shared__ float part[NT > 64 ? NT / 64 : 1];
+  const int t = threadIdx.x % NT;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / NT;
+  const bool live = row0 < a.rows;
+  const int64_t row = live ? row0 : a.rows - 1;
+  const int d = a.d;
+  const bool vec = d % 8 == 0;
+  const size_t base = static_cast<size_t>(row) * d;
+
+  float v[kChunks][8];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+    load8(static_cast<const TI *>(a.x) + base, (c * NT + t) * 8, d, vec, v[c]);
+  if (NORM && a.residual) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float s[8];
+      load8(static_cast<const TI *>(a.residual) + base, (c * NT + t) * 8, d, vec, s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] += s[i];
+      if (a.r && live)
+        store8(static_cast<TI *>(a.r) + base, (c * NT + t) * 8, d, vec, v[c]);
+    }
+  }
+  if constexpr (NORM) {
+    // the norm takes the unrounded sum
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss[0] = fmaf(v[c][i], v[c][i], ss[0]);
+    row_reduce<NT, 1, Add>(ss, part);
+    const float rs = rsqrtf(ss[0] / static_cast<float>(d) + a.eps);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float w[8] = {};
+      if (a.norm_w) load8(a.norm_w, (c * NT + t) * 8, d, vec, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * rs * (1.0f + w[i]);
+    }
+  }
+  if constexpr (__is_same(TO, e4m3_t)) {
+    float top[1] = {kTinyMax};
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[0] = max_nan(top[0], fabsf(v[c][i]));
+    row_reduce<NT, 1, Max>(top, part);
+    if (live && t == 0) a.y_scale[row] = top[0] / kE4m3Max;
+    const float inv = kE4m3Max / top[0];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= inv;
+  }
+  if (!live) return;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c)
+    store8(static_cast<TO *>(a.y) + base, (c * NT + t) * 8, d, vec, v[c]);
+}
+
+// Backward: a workgroup takes rows block, block + gridDim, ... (RPB of them at
+// a time) and keeps the weight gradient of its rows in registers; the
+// per-workgroup sums go to a.part [gridDim][d], added in order by
+// colsum_kernel.
+template <typename TI, typename TG, int NT>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int RPB = NT < 256 ? 256 / NT : 1;
+  __shared__ float part[NT > 64 ? 2 * (NT / 64) : 1];
+  __shared__ float join[RPB > 1 ? RPB * NT * kChunks * 8 : 1];
+  const int t = threadIdx.x % NT, grp = threadIdx.x / NT;
+  const int d = a.d;
+  const bool vec = d % 8 == 0;
+  float acc[kChunks][8] = {};
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * RPB; r0 < a.rows;
+       r0 += static_cast<int64_t>(gridDim.x) * RPB) {
+    const bool live = r0 + grp < a.rows;
+    const size_t base = static_cast<size_t>(live ? r0 + grp : a.rows - 1) * d;
+    float r[kChunks][8], g[kChunks][8];
+    float sum[2] = {0.0f, 0.0f};  // sum r^2, sum g r
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int e0 = (c * NT + t) * 8;
+      load8(static_cast<const TI *>(a.r) + base, e0, d, vec, r[c]);
+      load8(static_cast<const TG *>(a.dy) + base, e0, d, vec, g[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      float w[8] = {};
+      if (a.norm_w) load8(a.norm_w, (c * NT + t) * 8, d, vec, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[0] = fmaf(r[c][i], r[c][i], sum[0]);
+        sum[1] = fmaf(g[c][i] * (1.0f + w[i]), r[c][i], sum[1]);
+      }
+    }
+    row_reduce<NT, 2, Add>(sum, part);
+    const float rs = rsqrtf(sum[0] / static_cast<float>(d) + a.eps);
+    const float along = rs * rs * sum[1] / static_cast<float>(d);
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int e0 = (c * NT + t) * 8;
+        float w[8] = {}, dx[8] = {};
+        if (a.norm_w) load8(a.norm_w, e0, d, vec, w);
+        if (a.dr) load8(static_cast<const TI *>(a.dr) + base, e0, d, vec, dx);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[c][i] = fmaf(g[c][i], r[c][i] * rs, acc[c][i]);
+          dx[i] += rs * (g[c][i] * (1.0f + w[i]) - r[c][i] * along);
+        }
+        store8(static_cast<TI *>(a.dx) + base, e0, d, vec, dx);
+      }
+    }
+  }
+  if (!a.part) return;
+  float *out = a.part + static_cast<size_t>(blockIdx.x) * d;
+  if constexpr (RPB > 1) {
+    constexpr int W = NT * kChunks * 8;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) join[grp * W + (c * NT + t) * 8 + i] = acc[c][i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < d; e += 256) {
+      float s = join[e];
+      for (int q = 1; q < RPB; ++q) s += join[q * W + e];
+      out[e] = s;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int e = (c * NT + t) * 8 + i;
+        if (e < d) out[e] = acc[c][i];
+      }
+  }
+}
+
+// out[c] = sum over p of part[p][c], in order: 32 columns per workgroup, the
+// rows dealt to 32 groups of threads and joined in a fixed tree
+__global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ part, int P, int d,
+                                                      float *__restrict__ out) {
+  __shared__ float s[32][33];
+  const int c = threadIdx.x % 32, g = threadIdx.x / 32;
+  const int col = blockIdx.x * 32 + c;
+  float v = 0.0f;
+  if (col < d)
+    for (int p = g; p < P; p += 32) v += part[static_cast<size_t>(p) * d + col];
+  s[g][c] = v;
+  __syncthreads();
+  if (g == 0 && col < d) {
+    for (int q = 1; q < 32; ++q) v += s[q][c];
+    out[col] = v;
+  }
+}
+
+template <typename F>
+hipError_t with_type(int code, F &&f) {
+  switch (code) {
+    case 1: return f(bf16_t{});
+    case 2: return f(_Float16{});
+    default: return f(float{});
+  }
+}
+
+// threads per row: the fewest whose registers hold it
+template <typename F>
+hipError_t with_threads(int d, F &&f) {
+  if (d <= 16 * 8 * kChunks) return f(std::integral_constant<int, 16>{});
+  if (d <= 64 * 8 * kChunks) return f(std::integral_constant<int, 64>{});
+  if (d <= 256 * 8 * kChunks) return f(std::integral_constant<int, 256>{});
+  return f(std::integral_constant<int, 1024>{});
+}
+static_assert(kNormMaxD == 1024 * 8 * kChunks, "widest row");
+
+template <bool NORM, typename TI, typename TO>
+hipError_t launch_rows(const NormArgs &a) {
+  return with_threads(a.d, [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    constexpr int RPB = NT < 256 ? 256 / NT : 1;
+    hipLaunchKernelGGL((rmsnorm_kernel<TI, TO, NT, NORM>),
+                       dim3(static_cast<unsigned>((a.rows + RPB - 1) / RPB)),
+                       dim3(NT < 256 ? 256 : NT), 0, a.stream, a);
+    return hipGetLastError();
+  });
+}
+
+// workgroups of the backward, and so partial sums of the weight gradient
+int bwd_blocks(int64_t rows, int d) {
+  int64_t b = 0;
+  with_threads(d, [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    constexpr int RPB = NT < 256 ? 256 / NT : 1;
+    b = (rows + RPB - 1) / RPB;
+    return hipSuccess;
+  });
+  return static_cast<int>(b < 512 ? b : 512);
+}
+
+}  // namespace
+
+hipError_t launch_colsum(const float *part, int P, int d, float *out, hipStream_t stream) {
+  hipLaunchKernelGGL(colsum_kernel, dim3((d + 31) / 32), dim3(1024), 0, stream, part, P, d, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_add_rmsnorm(const NormArgs &a) {
+  if (a.rows == 0) return hipSuccess;
+  return with_type(a.in_dtype, [&](auto ti) {
+    using TI = decltype(ti);
+    if (a.out_dtype == kE4m3) return launch_rows<true, TI, e4m3_t>(a);
+    return with_type(a.out_dtype,
+                     [&](auto to) { return launch_rows<true, TI, decltype(to)>(a); });
+  });
+}
+
+hipError_t launch_quantize_rows(const NormArgs &a) {
+  if (a.rows == 0) return hipSuccess;
+  return with_type(a.in_dtype, [&](auto ti) { return launch_rows<false, decltype(ti), e4m3_t>(a); });
+}
+
+size_t add_rmsnorm_bwd_workspace_size(int64_t rows, int d) {
+  return static_cast<size_t>(bwd_blocks(rows, d)) * d * 4;
+}
+
+hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs &a) {
+  const int P = bwd_blocks(a.rows, a.d);
+  if (P > 0) {
+    const hipError_t e = with_type(a.in_dtype, [&](auto ti) {
+      return with_type(a.dy_dtype, [&](auto tg) {
+        return with_threads(a.d, [&](auto nt) {
+          constexpr int NT = decltype(nt)::value;
+          hipLaunchKernelGGL((rmsnorm_bwd_kernel<decltype(ti), decltype(tg), NT>), dim3(P),
+                             dim3(NT < 256 ? 256 : NT), 0, a.stream, a);
+          return hipGetLastError();
+        });
+      });
+    });
+    if (e != hipSuccess) return e;
+  }
+  return a.dnorm_w ? launch_colsum(a.part, P, a.d, a.dnorm_w, a.stream) : hipSuccess;
+}
+
+}  // namespace gdn

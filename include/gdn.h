@@ -56,6 +56,17 @@ enum gdn_dtype_e {
   GDN_F32 = 0,
   GDN_BF16 = 1,
   GDN_F16 = 2,
+  /* 8 bits, 4 exponent and 3 mantissa, no infinities, largest value 448; only
+   * where a call names it */
+  GDN_E4M3 = 3,
+};
+
+/* activations of gdn_linear */
+enum gdn_act_e {
+  GDN_ACT_NONE = 0,
+  GDN_ACT_SILU = 1,    /* u / (1 + exp(-u)) */
+  GDN_ACT_GELU = 2,    /* u (1 + erf(u / sqrt(2))) / 2 */
+  GDN_ACT_SIGMOID = 3, /* 1 / (1 + exp(-u)) */
 };
 
 /* return codes */
@@ -499,6 +510,144 @@ GDN_API int gdn_conv_state_from_prefill(const void *q_raw, const void *k_raw,
                                         const int32_t *slot_idx, int32_t n_slots,
                                         void *conv_state, int32_t dtype,
                                         void *stream);
+
+/*
+ * The layer around the mixer. A layer adds the block's output to the residual
+ * stream and normalises it, projects it to the mixer's streams (page "NLP——
+ * 技术报告解读-Qwen3.8-Flash-Next", section "GDN 参数化细节": W_q, W_k, W_v,
+ * W_alpha, W_beta, W_z), and projects the mixer's output back (W_o) into the
+ * residual stream. The calls below are those steps and their gradients:
+ * tensors are row-major and contiguous, rows are tokens.
+ */
+
+/*
+ * Residual addition and RMSNorm, with the zero-centred gain of the output
+ * gate:
+ *     r = x + residual
+ *     y = r / sqrt(mean(r^2) + rms_eps) * (1 + norm_w)      per row of d
+ *
+ *   x         [rows, d] in in_dtype.
+ *   residual  [rows, d] in in_dtype, or NULL: r = x.
+ *   norm_w    float32 [d], or NULL for zeros.
+ *   r         [rows, d] in in_dtype: the new residual stream; NULL to skip,
+ *             and NULL without a residual. May be x or residual itself (in
+ *             place), must not overlap anything else.
+ *   y         [rows, d] in out_dtype. GDN_E4M3: per row
+ *             scale = max(max |y|, 1e-30) / 448, the row is y / scale rounded
+ *             to the nearest e4m3 value, ties to even.
+ *   y_scale   float32 [rows], with GDN_E4M3 only: the scales; else NULL.
+ *   rows >= 0, 1 <= d <= 32768 (GDN_ERR_UNSUPPORTED above).
+ * The norm takes the unrounded sum. A row that holds an infinity or NaN gives
+ * NaN in y where the formula does (and as its scale, if a NaN is in y).
+ * Any d; multiples of 8 use vector accesses. The tensors and norm_w are
+ * 16-byte aligned, y_scale 4-byte.
+ */
+GDN_API int gdn_add_rmsnorm(const void *x, const void *residual,
+                            const float *norm_w, float rms_eps, void *r,
+                            void *y, float *y_scale, int64_t rows, int32_t d,
+                            int32_t in_dtype, int32_t out_dtype, void *stream);
+
+/*
+ * Rows to 8 bits, for gdn_linear's weights and inputs: per row
+ * y_scale = max(max |x|, 1e-30) / 448 and y = x / y_scale rounded to the
+ * nearest e4m3 value. x [rows, d] in in_dtype, y [rows, d] e4m3, y_scale
+ * float32 [rows]; sizes and alignment as gdn_add_rmsnorm.
+ */
+GDN_API int gdn_quantize_rows(const void *x, void *y, float *y_scale,
+                              int64_t rows, int32_t d, int32_t in_dtype,
+                              void *stream);
+
+/*
+ * Backward of gdn_add_rmsnorm: the gradients of
+ *     L = <dy, y> + <dr, r>
+ * with respect to r (which is the gradient of x and of residual alike) and
+ * norm_w. The row sums are taken again from r; nothing is kept from the
+ * forward.
+ *
+ *   dy       [rows, d] in dy_dtype (GDN_F32, GDN_BF16 or GDN_F16).
+ *   r        [rows, d] in in_dtype: the forward's r, or its x without a
+ *            residual.
+ *   dr       [rows, d] in in_dtype: gradient that reaches r by another way
+ *            (the residual stream), or NULL for zeros.
+ *   norm_w   as in the forward.
+ *   dx       [rows, d] in in_dtype; may be dr itself (in place).
+ *   dnorm_w  float32 [d], or NULL to skip; zeros when rows is 0.
+ *   workspace  device memory, 256-byte aligned, of at least
+ *            gdn_add_rmsnorm_bwd_workspace_size(rows, d) bytes, overwritten
+ *            (not used without dnorm_w, may then be NULL): partial sums of
+ *            dnorm_w, added in a fixed order.
+ */
+GDN_API size_t gdn_add_rmsnorm_bwd_workspace_size(int64_t rows, int32_t d);
+GDN_API int gdn_add_rmsnorm_bwd(const void *dy, const void *r, const void *dr,
+                                const float *norm_w, float rms_eps, void *dx,
+                                float *dnorm_w, int64_t rows, int32_t d,
+                                int32_t in_dtype, int32_t dy_dtype,
+                                void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
+ * Matrix product with its epilogue:
+ *     u = x w^T + bias            y = act(u) + residual
+ *
+ *   x        [M, K], w [N, K], both in in_dtype: GDN_F32, GDN_BF16, GDN_F16 or
+ *            GDN_E4M3. With GDN_E4M3, x_scale float32 [M] and w_scale float32
+ *            [N] are required and u = (x w^T) x_scale[m] w_scale[n] + bias;
+ *            with the other types both are NULL. Products and sums are fp32
+ *            (fp32 inputs: fp32 matrix instructions), with one exception:
+ *            GDN_E4M3 inputs with a 16-bit output may use the 8-bit matrix
+ *            instructions, which cut each product off 13 bits below the
+ *            largest of its group of 8 (relative error of u about 1.5e-5).
+ *   bias     float32 [N], or NULL for zeros.
+ *   act      gdn_act_e.
+ *   residual [M, N] in out_dtype, or NULL for zeros.
+ *   pre      [M, N] in out_dtype: u, for gdn_linear_bwd; NULL to skip.
+ *   y        [M, N] in out_dtype (GDN_F32, GDN_BF16 or GDN_F16). May be
+ *            residual itself (in place), must not overlap anything else.
+ *   M >= 0 (0: nothing is written), N, K >= 1; a row of K or N elements of
+ *            in_dtype is at most 8 MiB.
+ *   workspace  device memory, 256-byte aligned, of at least
+ *            gdn_linear_workspace_size(M, N, K, in_dtype) bytes, overwritten
+ *            (NULL where that is 0): partial sums where few output tiles make
+ *            the reduction worth splitting, and padded copies of x and w where
+ *            a row of K elements is no whole number of 16-byte vectors.
+ * The tensors, bias and w_scale are 16-byte aligned, x_scale 4-byte.
+ */
+GDN_API size_t gdn_linear_workspace_size(int64_t M, int32_t N, int32_t K,
+                                         int32_t in_dtype);
+GDN_API int gdn_linear(const void *x, const float *x_scale, const void *w,
+                       const float *w_scale, const float *bias,
+                       const void *residual, void *pre, void *y, int64_t M,
+                       int32_t N, int32_t K, int32_t act, int32_t in_dtype,
+                       int32_t out_dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * Backward of gdn_linear: with du = dy act'(pre),
+ *     dx = du w      dw = du^T x      dbias = sum over rows of du
+ * (the residual's gradient is dy itself).
+ *
+ *   dy, pre  [M, N] in dy_dtype, the forward's out_dtype; pre is required with
+ *            an activation and not read without one.
+ *   x, w     the forward's inputs, GDN_F32, GDN_BF16 or GDN_F16 (x is read for
+ *            dw, w for dx).
+ *   dx       [M, K], dw [N, K], both in in_dtype, and dbias float32 [N]: each
+ *            NULL to skip it. With M = 0, dw and dbias are zeros.
+ *   workspace  device memory, 256-byte aligned, of at least
+ *            gdn_linear_bwd_workspace_size(M, N, K, act, in_dtype, dy_dtype)
+ *            bytes, overwritten: du where it differs from dy, operands laid
+ *            out for the products, partial sums.
+ * The products take du rounded to in_dtype (as the matrix cores need it) and
+ * sum in fp32; dbias sums the unrounded du. Sizes as gdn_linear, and a column
+ * of M elements is at most 8 MiB. Sums are added in a fixed order.
+ */
+GDN_API size_t gdn_linear_bwd_workspace_size(int64_t M, int32_t N, int32_t K,
+                                             int32_t act, int32_t in_dtype,
+                                             int32_t dy_dtype);
+GDN_API int gdn_linear_bwd(const void *dy, const void *pre, const void *x,
+                           const void *w, void *dx, void *dw, float *dbias,
+                           int64_t M, int32_t N, int32_t K, int32_t act,
+                           int32_t in_dtype, int32_t dy_dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 /* Human-readable name of a return code (static string, never NULL). */
 GDN_API const char *gdn_status_string(int status);
