@@ -27,11 +27,14 @@ FLAGS = [
     "-ffp-contract=fast",
     # keep hipcc from emitting packed fp32 arithmetic in device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA accumulators in ordinary VGPRs: avoids AGPR<->VGPR copies around
-    # loop-carried accumulators
-    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-I", os.path.join(os.path.dirname(HERE), "include"),
 ]
+
+# MFMA accumulators in ordinary VGPRs: avoids AGPR<->VGPR copies around
+# loop-carried accumulators
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+# linear.hip's large tile fills the accumulation registers instead
+ACC_IN_AGPRS = {"linear.hip"}
 
 
 def sources():
@@ -40,7 +43,8 @@ def sources():
 
 def _compile(src):
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [HIPCC] + FLAGS + ["-c", src, "-o", obj]
+    form = [] if os.path.basename(src) in ACC_IN_AGPRS else VGPR_FORM
+    cmd = [HIPCC] + FLAGS + form + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     out = "\n".join(l for l in r.stdout.splitlines() if "packed-fp32-ops" not in l)
     if r.returncode != 0:

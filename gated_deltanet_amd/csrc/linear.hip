@@ -9,6 +9,8 @@
 // 16-byte vectors apart. Operands that are not laid out so (odd widths, the
 // transposes that the backward reduces over) are first copied into the
 // workspace, padded with zeros.
+#include <type_traits>
+
 #include "gdn_device.h"
 #include "gdn_internal.h"
 
@@ -16,6 +18,7 @@ namespace gdn {
 namespace {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kTile = 128;  // output tile of a workgroup
 constexpr int kStep = 128;  // bytes of the reduction axis per step
@@ -63,6 +66,7 @@ template <typename T>
 struct Vec4;
 template <>
 struct Vec4<float> {
+  typedef f32x4 raw;
   __device__ static __forceinline__ f32x4 load(const float *p) {
     return *reinterpret_cast<const f32x4 *>(p);
   }
@@ -72,6 +76,7 @@ struct Vec4<float> {
 };
 template <>
 struct Vec4<_Float16> {
+  typedef f16x4 raw;
   __device__ static __forceinline__ f32x4 load(const _Float16 *p) {
     return __builtin_convertvector(*reinterpret_cast<const f16x4 *>(p), f32x4);
   }
@@ -82,6 +87,7 @@ struct Vec4<_Float16> {
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 template <>
 struct Vec4<bf16_t> {
+  typedef bf16x4 raw;
   __device__ static __forceinline__ f32x4 load(const bf16_t *p) {
     return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(p), f32x4);
   }
@@ -203,7 +209,6 @@ __device__ __forceinline__ f32x4 mma_step(const u32x4 (&a)[2], const u32x4 (&b)[
                                                      widen_e4m3(b[h][2 * q], b[h][2 * q + 1]), acc,
                                                      0, 0, 0);
   } else {
-    typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
     struct Pair {
       u32x4 v[2];
     };
@@ -212,6 +217,51 @@ __device__ __forceinline__ f32x4 mma_step(const u32x4 (&a)[2], const u32x4 (&b)[
         acc, 0, 0, 0, 0, 0, 0);  // e4m3 by e4m3, no block scales
   }
   return acc;
+}
+
+// One matrix instruction of mma_step with the accumulator updated in place:
+// part 0 or 1 (8-bit types have one part). Written in asm, with the
+// accumulator in the accumulation registers: from the builtins the compiler
+// moves accumulators between registers around a kernel that fills them all.
+// The compiler knows no wait states around it: s_nop 1 covers operands that
+// were just written by a VALU instruction, and settle() below has to stand
+// between the last product and any other use of the accumulators.
+template <typename T>
+__device__ __forceinline__ void mma_part(const i32x8 &a, const i32x8 &b, f32x4 &acc, int part) {
+  if constexpr (__is_same(T, e4m3_t)) {
+    asm("s_nop 1\n\tv_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+  } else {
+    const i32x4 a4 = part ? __builtin_shufflevector(a, a, 4, 5, 6, 7)
+                          : __builtin_shufflevector(a, a, 0, 1, 2, 3);
+    const i32x4 b4 = part ? __builtin_shufflevector(b, b, 4, 5, 6, 7)
+                          : __builtin_shufflevector(b, b, 0, 1, 2, 3);
+    if constexpr (__is_same(T, bf16_t))
+      asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a4), "v"(b4));
+    else
+      asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a4), "v"(b4));
+  }
+}
+__device__ __forceinline__ void settle(f32x4 (&c)[8]) {
+  asm volatile("s_nop 15\n\ts_nop 3"
+               : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]),
+                 "+a"(c[6]), "+a"(c[7]));
+}
+
+// Workgroups are dealt round robin to the 8 XCDs, each with an L2 of its own:
+// XCD x takes a run of consecutive tiles, ordered so that the 32 tiles that
+// its CUs work on at a time are 8 row tiles by 4 column tiles.
+struct TileAt {
+  int64_t m;
+  int n;
+};
+__device__ __forceinline__ TileAt tile_at(int64_t tiles_m, int tiles_n) {
+  const uint32_t total = gridDim.x, x = blockIdx.x % 8, slot = blockIdx.x / 8;
+  const uint32_t q = total / 8, r = total % 8;
+  const uint32_t t = x * q + (x < r ? x : r) + slot;
+  const uint32_t group = t / (8 * tiles_n), in = t % (8 * tiles_n);
+  const int64_t left = tiles_m - static_cast<int64_t>(group) * 8;
+  const uint32_t rows = left < 8 ? static_cast<uint32_t>(left) : 8;
+  return {static_cast<int64_t>(group) * 8 + in % rows, static_cast<int>(in / rows)};
 }
 
 struct GemmArgs {
@@ -223,6 +273,7 @@ struct GemmArgs {
   int steps;                 // kStep-byte steps per split
   float *part;               // null: epilogue; else [splits][M][ldpart] sums
   int64_t ldpart;
+  int64_t tiles_m;
   int tiles_n;
   Epilogue e;
 };
@@ -238,8 +289,9 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lc = lane % 16, lg = lane / 16;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x / g.tiles_n) * kTile;
-  const int n0 = static_cast<int>(blockIdx.x % g.tiles_n) * kTile;
+  const TileAt at = tile_at(g.tiles_m, g.tiles_n);
+  const int64_t m0 = at.m * kTile;
+  const int n0 = at.n * kTile;
   const int wm = (wave / 2) * 64, wn = (wave % 2) * 64;
 
   // rows past the operand's end lie past the resource's end and read as zeros
@@ -313,6 +365,286 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
       else
         epilogue4(g.e, m, n, acc[i][j]);
     }
+  }
+}
+
+__device__ __forceinline__ float readlane(float x, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l));
+}
+
+// Epilogue of 8 rows of C, m .. m + 7, by one wave: columns n .. n + 3 of each
+// per lane, the products in LDS at rows + r * ldc, the residual in registers.
+// Rows are uniform, so their addresses are scalar.
+template <typename TO, int ACT>
+__device__ __forceinline__ void epilogue_rows8(const Epilogue &e, const float *rows, int ldc,
+                                               int64_t m, int n, float xs, int xlane, f32x4 ws,
+                                               f32x4 b, const typename Vec4<TO>::raw (&res)[8]) {
+  f32x4 v[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const f32x4 *>(rows + r * ldc);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    if (m + r >= e.M) break;
+    if (e.w_scale) {
+      const float x = readlane(xs, xlane + r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[r][i] *= x * ws[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[r][i] += b[i];
+    if (e.pre) {
+      TO *to = static_cast<TO *>(e.pre) + (m + r) * e.N;
+      Vec4<TO>::store(to + n, v[r]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[r][i] = act_fwd(v[r][i], ACT);
+    if (e.residual) {
+      const f32x4 x = __builtin_convertvector(res[r], f32x4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[r][i] += x[i];
+    }
+    TO *to = static_cast<TO *>(e.y) + (m + r) * e.N;
+    Vec4<TO>::store(to + n, v[r]);
+    // an activation's rows one after the other: side by side they would spill
+    if (ACT) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Epilogue of one wave's part of a tile, N a multiple of 4: `halves` times 32
+// rows, from row m + hstep * half, staged to LDS at `rows` by stage(half). The
+// residual of 8 rows is requested while the 8 before them are worked on.
+template <typename TO, typename F>
+__device__ __forceinline__ void epilogue_wave(const Epilogue &e, const float *rows, int ldc,
+                                              int64_t m, int hstep, int n, F &&stage) {
+  typedef typename Vec4<TO>::raw raw;
+  const bool in = n < e.N;
+  f32x4 ws = zero4(), b = zero4();
+  if (in && e.w_scale) ws = Vec4<float>::load(e.w_scale + n);
+  if (in && e.bias) b = Vec4<float>::load(e.bias + n);
+  // x_scale of row r of half h in lane 32 h + r
+  float xs = 0.0f;
+  if (e.w_scale) {
+    const int lane = threadIdx.x % 64;
+    const int64_t row = m + hstep * (lane / 32) + lane % 32;
+    xs = e.x_scale[row < e.M ? row : e.M - 1];
+  }
+  raw res[8], next[8];
+  auto fetch = [&](int64_t at) {
+    if (!e.residual || !in) return;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int64_t row = at + r < e.M ? at + r : e.M - 1;
+      const TO *from = static_cast<const TO *>(e.residual) + row * e.N;
+      next[r] = *reinterpret_cast<const raw *>(from + n);
+    }
+  };
+  fetch(m);
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    stage(half);
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      const int64_t at = m + hstep * half + 8 * q;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) res[r] = next[r];
+      if (q < 3) fetch(at + 8);
+      else if (half == 0) fetch(m + hstep);
+      if (!in) continue;
+      const float *from = rows + 8 * q * ldc;
+      const int xl = 32 * half + 8 * q;
+      switch (e.act) {
+        case 1: epilogue_rows8<TO, 1>(e, from, ldc, at, n, xs, xl, ws, b, res); break;
+        case 2: epilogue_rows8<TO, 2>(e, from, ldc, at, n, xs, xl, ws, b, res); break;
+        case 3: epilogue_rows8<TO, 3>(e, from, ldc, at, n, xs, xl, ws, b, res); break;
+        default: epilogue_rows8<TO, 0>(e, from, ldc, at, n, xs, xl, ws, b, res); break;
+      }
+    }
+  }
+}
+
+// The large tile: 256 x 256 of C by four waves, each 128 x 128 of it (256
+// accumulator registers), so that a step's LDS reads (4 x 32 KB) and direct
+// loads (64 KB) take 1536 of the 2048 clocks its products take at the 128
+// bytes a clock of LDS. One wave per SIMD: nothing hides a stall but the wave
+// itself, so everything is ordered by hand. A step of 128 bytes of the
+// reduction axis is four quadrants of 64 x 64; A0, A1 (halves of the wave's
+// rows of q) and B0, B1 (of p) are read one quadrant before their first use,
+// the halves of B in turn first and second so that no register is held twice:
+//     (A0 Bf) read Bs | (A0 Bs) read A1 | barrier | (A1 Bs) read A0' | (A1 Bf) read Bs'
+// where ' is the next step, whose Bf is this one's Bs. At the barrier the next
+// stage has landed and this one is fully read: the stage after next is loaded
+// over it, a whole step (about 1 us) ahead of its use.
+// Row groups 4 HALF .. 4 HALF + 3 of the accumulators to LDS, straight from
+// the accumulation registers (the barrier that follows waits for it).
+template <int HALF, int LDC>
+__device__ __forceinline__ void store_half(uint32_t to, const f32x4 (&acc)[8][8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(to), "a"(acc[i][4 * HALF + j]),
+                   "n"((16 * j * LDC + 16 * i) * 4)
+                   : "memory");
+}
+
+struct Half {
+  i32x8 v[4];
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
+gemm256_kernel(const GemmArgs g) {
+  constexpr int TILE = 256, STAGE = 2 * TILE * kStep, LDC = TILE + 4;
+  constexpr int PARTS = __is_same(T, e4m3_t) ? 1 : 2;  // instructions per tile and step
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE + 128 * 16];
+  static_assert(sizeof(smem) >= 128 * LDC * 4, "half a tile of fp32 for the epilogue");
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int lc = lane % 16, lg = lane / 16;
+  const TileAt at = tile_at(g.tiles_m, g.tiles_n);
+  const int64_t m0 = at.m * TILE;
+  const int n0 = at.n * TILE;
+  const int wm = (wave / 2) * 128, wn = (wave % 2) * 128;
+
+  const int64_t mrows = g.M - m0 < TILE ? g.M - m0 : TILE;
+  const int nrows = g.N - n0 < TILE ? g.N - n0 : TILE;
+  const i32x4 rp = buffer_rsrc(g.p + m0 * g.ldp, static_cast<uint32_t>(mrows * g.ldp));
+  const i32x4 rq = buffer_rsrc(g.q + n0 * g.ldq, static_cast<uint32_t>(nrows * g.ldq));
+
+  const int row = lane / 8;
+  const int vecoff = ((lane % 8) ^ row) * 16;
+  const int s0 = blockIdx.y * g.steps;
+  const int total = (g.rbytes + kStep - 1) / kStep;
+  const int s1 = s0 + g.steps < total ? s0 + g.steps : total;
+  uint32_t op[8], oq[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    op[i] = static_cast<uint32_t>(((wave + 4 * i) * 8 + row) * g.ldp);
+    oq[i] = static_cast<uint32_t>(((wave + 4 * i) * 8 + row) * g.ldq);
+  }
+  const uint32_t lds0 = lds_addr(smem);
+  // load i (0..7: p, 8..15: q) of step s; past the split or the axis it reads zeros
+  auto offset = [&](int s) {
+    const int r = s * kStep + vecoff;
+    return s < s1 && r < g.rbytes ? static_cast<uint32_t>(r) : 0x80000000u;
+  };
+  auto load = [&](uint32_t r, int buf, int i) {
+    const uint32_t at = lds0 + buf * STAGE + (i < 8 ? 0 : TILE * kStep) + (wave + 4 * (i % 8)) * 1024;
+    if (i < 8) dma16(rp, op[i] + r, at);
+    else dma16(rq, oq[i - 8] + r, at);
+  };
+
+  const int o0 = lc * 128 + ((lg ^ (lc & 7)) * 16);
+  // 16 bytes of one half's fragments: vector i % 2 of row group i / 2, i = 0..7
+  auto read = [&](Half &f, int at, int i) {
+    const i32x4 x = *reinterpret_cast<const i32x4 *>(smem + at + 16 * (i / 2) * 128 +
+                                                     (o0 ^ (64 * (i % 2))));
+    i32x8 &d = f.v[i / 2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[4 * (i % 2) + e] = x[e];
+  };
+  auto read_a = [&](Half &f, int buf, int h, int i) {
+    read(f, buf * STAGE + TILE * kStep + (wn + 64 * h) * 128, i);
+  };
+  auto read_b = [&](Half &f, int buf, int h, int i) {
+    read(f, buf * STAGE + (wm + 64 * h) * 128, i);
+  };
+
+  f32x4 acc[8][8];  // [n tile][m tile]
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = zero4();
+
+  // one quadrant, with `side(0..7)` spread between its products
+  auto quadrant = [&](const Half &a, const Half &b, int ia, int jb, auto &&side) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        mma_part<T>(a.v[t / 4], b.v[t % 4], acc[4 * ia + t / 4][4 * jb + t % 4], p);
+        constexpr int EVERY = 2 * PARTS;
+        if ((p * 16 + t) % EVERY == EVERY - 1) {
+          side((p * 16 + t) / EVERY);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+  };
+
+  Half A0, A1, B0, B1;
+  auto step = [&](int s, auto par) {
+    constexpr int P = decltype(par)::value;  // stage, and which half of B comes first
+    Half &Bf = P ? B1 : B0, &Bs = P ? B0 : B1;
+    quadrant(A0, Bf, 0, P, [&](int i) { read_b(Bs, P, 1 - P, i); });
+    quadrant(A0, Bs, 0, 1 - P, [&](int i) { read_a(A1, P, 1, i); });
+    wait_vmcnt<0>();
+    wg_barrier();
+    const uint32_t r = offset(s + 2);
+    quadrant(A1, Bs, 1, 1 - P, [&](int i) {
+      read_a(A0, 1 - P, 0, i);
+      load(r, P, i);
+    });
+    quadrant(A1, Bf, 1, P, [&](int i) {
+      read_b(Bs, 1 - P, 1 - P, i);
+      load(r, P, 8 + i);
+    });
+  };
+
+  if (s0 < s1) {
+    const uint32_t r0 = offset(s0), r1 = offset(s0 + 1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) load(r0, 0, i);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) load(r1, 1, i);
+    wait_vmcnt<16>();
+    wg_barrier();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) read_a(A0, 0, 0, i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) read_b(B0, 0, 0, i);
+    // an odd count ends with a step of zeros
+    for (int s = s0; s < s1; s += 2) {
+      step(s, std::integral_constant<int, 0>{});
+      step(s + 1, std::integral_constant<int, 1>{});
+    }
+    wait_vmcnt<0>();  // no load may land in LDS that is used otherwise, or by others
+  }
+
+#pragma unroll
+  for (int i = 0; i < 8; ++i) settle(acc[i]);
+
+  // Half of the rows of C at a time through LDS, so that the stores (and the
+  // reads of bias and residual) are whole rows of 256 columns: rows 0..63 of
+  // the LDS tile are those of waves 0 and 1, 64..127 of waves 2 and 3, and
+  // each wave then takes 32 of the 128.
+  float *cs = reinterpret_cast<float *>(smem);
+  auto stage = [&](int half) {
+    wg_barrier();
+    const uint32_t to = lds0 + ((wm / 2 + lc) * LDC + wn + 4 * lg) * 4;
+    if (half == 0) store_half<0, LDC>(to, acc);
+    else store_half<1, LDC>(to, acc);
+    wg_barrier();
+  };
+  const int n = n0 + 4 * lane;
+  const int64_t m = m0 + (wave / 2) * 128 + (wave % 2) * 32;  // row of `rows`, + 64 in half 1
+  const float *rows = cs + 32 * wave * LDC + 4 * lane;
+  if (g.part || g.N % 4 != 0) {
+    for (int half = 0; half < 2; ++half) {
+      stage(half);
+      if (n >= g.N) continue;
+      float *out = g.part + (static_cast<size_t>(blockIdx.y) * g.M + m + 64 * half) * g.ldpart + n;
+      for (int r = 0; r < 32 && m + 64 * half + r < g.M; ++r) {
+        const f32x4 v = *reinterpret_cast<const f32x4 *>(rows + r * LDC);
+        if (g.part) *reinterpret_cast<f32x4 *>(out + r * g.ldpart) = v;
+        else epilogue4(g.e, m + 64 * half + r, n, v);
+      }
+    }
+  } else if (g.e.out_dtype == 1) {
+    epilogue_wave<bf16_t>(g.e, rows, LDC, m, 64, n, stage);
+  } else if (g.e.out_dtype == 2) {
+    epilogue_wave<_Float16>(g.e, rows, LDC, m, 64, n, stage);
+  } else {
+    epilogue_wave<float>(g.e, rows, LDC, m, 64, n, stage);
   }
 }
 
@@ -410,6 +742,7 @@ hipError_t with_type(int code, F &&f) {
 
 // One product: how the reduction is split and what that needs.
 struct GemmPlan {
+  int tile;
   int64_t tiles_m;
   int tiles_n;
   int splits, steps;
@@ -419,10 +752,11 @@ struct GemmPlan {
 
 // Few output tiles leave CUs idle: the reduction is then split until about 256
 // workgroups run, each keeping at least four steps.
-GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes) {
+GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes, bool large) {
   GemmPlan p;
-  p.tiles_m = (M + kTile - 1) / kTile;
-  p.tiles_n = (N + kTile - 1) / kTile;
+  p.tile = large && M * N >= 64 * 256 * 256 ? 256 : kTile;
+  p.tiles_m = (M + p.tile - 1) / p.tile;
+  p.tiles_n = (N + p.tile - 1) / p.tile;
   const int total = static_cast<int>((rbytes + kStep - 1) / kStep);
   const int64_t tiles = p.tiles_m * p.tiles_n;
   int64_t want = tiles > 0 ? 256 / tiles : 1;
@@ -436,10 +770,14 @@ GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes) {
   return p;
 }
 
+// whether the large tile exists for the types: 16-bit and 8-bit matrix
+// instructions (fp32 sums of 8-bit operands are taken by the small one)
+bool large_ok(int dtype, int out_dtype) { return dtype != 0 && !(dtype == kE4m3 && out_dtype == 0); }
+
 hipError_t run_gemm(const void *P, int64_t ldp, const void *Q, int64_t ldq, int64_t M, int N,
                     int64_t rbytes, int dtype, const Epilogue &e, char *part, hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  const GemmPlan p = plan_gemm(M, N, rbytes);
+  const GemmPlan p = plan_gemm(M, N, rbytes, large_ok(dtype, e.out_dtype));
   GemmArgs g;
   g.p = static_cast<const char *>(P);
   g.q = static_cast<const char *>(Q);
@@ -451,10 +789,18 @@ hipError_t run_gemm(const void *P, int64_t ldp, const void *Q, int64_t ldq, int6
   g.steps = p.steps;
   g.part = p.splits > 1 ? reinterpret_cast<float *>(part) : nullptr;
   g.ldpart = p.ldpart;
+  g.tiles_m = p.tiles_m;
   g.tiles_n = p.tiles_n;
   g.e = e;
   const dim3 grid(static_cast<unsigned>(p.tiles_m * p.tiles_n), p.splits);
-  if (dtype == kE4m3 && e.out_dtype == 0)
+  if (p.tile == 256) {
+    if (dtype == kE4m3)
+      hipLaunchKernelGGL(gemm256_kernel<e4m3_t>, grid, dim3(256), 0, stream, g);
+    else if (dtype == 1)
+      hipLaunchKernelGGL(gemm256_kernel<bf16_t>, grid, dim3(256), 0, stream, g);
+    else
+      hipLaunchKernelGGL(gemm256_kernel<_Float16>, grid, dim3(256), 0, stream, g);
+  } else if (dtype == kE4m3 && e.out_dtype == 0)
     hipLaunchKernelGGL((gemm_kernel<e4m3_t, true>), grid, dim3(256), 0, stream, g);
   else if (dtype == kE4m3)
     hipLaunchKernelGGL((gemm_kernel<e4m3_t, false>), grid, dim3(256), 0, stream, g);
@@ -521,7 +867,9 @@ FwdLayout fwd_layout(int64_t M, int N, int K, int dtype) {
   L.w = off;
   if (L.pad) off += align256(static_cast<size_t>(N) * rb);
   L.part = off;
-  off += plan_gemm(M, N, rb).part_bytes;
+  const size_t p1 = plan_gemm(M, N, rb, false).part_bytes;
+  const size_t p2 = plan_gemm(M, N, rb, large_ok(dtype, 1)).part_bytes;
+  off += p1 > p2 ? p1 : p2;
   L.total = off;
   return L;
 }
@@ -558,7 +906,8 @@ BwdLayoutL bwd_layout(int64_t M, int N, int K, int act, int in_dtype, int dy_dty
   L.db = off;
   off += align256(static_cast<size_t>((M + du_run(M) - 1) / du_run(M)) * N * 4);
   L.part = off;
-  const size_t p1 = plan_gemm(M, K, rn).part_bytes, p2 = plan_gemm(N, K, rm).part_bytes;
+  const size_t p1 = plan_gemm(M, K, rn, large_ok(in_dtype, in_dtype)).part_bytes;
+  const size_t p2 = plan_gemm(N, K, rm, large_ok(in_dtype, in_dtype)).part_bytes;
   off += p1 > p2 ? p1 : p2;
   L.total = off;
   return L;

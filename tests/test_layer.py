@@ -339,6 +339,27 @@ def test_linear(M, N, K, dtype, out):
     _check_linear(M, N, K, dtype, out, "silu", True, True, True, seed=1)
 
 
+# enough output for the large tiles: partial tiles, a reduction that ends inside
+# a step, an odd number of steps, rows that no vector divides, a split reduction
+@gpu
+@pytest.mark.parametrize("M,N,K", [(2100, 2200, 328), (2100, 2201, 136), (4100, 1100, 64),
+                                   (2048, 2048, 4096), (2304, 2052, 24), (1900, 2500, 1155)])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32"), ("e4m3", "bf16"),
+                                       ("e4m3", "f16"), ("e4m3", "f32"), ("f32", "f32")])
+def test_linear_large_tiles(M, N, K, dtype, out):
+    _check_linear(M, N, K, dtype, out, "none", False, True, False)
+    _check_linear(M, N, K, dtype, out, "gelu", True, False, True, seed=1)
+    _check_linear(M, N, K, dtype, out, "silu", True, True, False, seed=2)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(2100, 264, 2200), (2100, 2056, 1112), (512, 2100, 2100)])
+@pytest.mark.parametrize("dtype,gtype,act", [("bf16", "bf16", "silu"), ("f16", "f16", "none"),
+                                             ("bf16", "f32", "none"), ("f32", "f32", "none")])
+def test_linear_bwd_large_tiles(M, N, K, dtype, gtype, act):
+    _check_linear_bwd(M, N, K, dtype, gtype, act)
+
+
 @gpu
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "sigmoid"])
 @pytest.mark.parametrize("dtype,out", [("bf16", "f16"), ("f32", "f32"), ("e4m3", "f32")])
