@@ -1205,8 +1205,7 @@ GDN_API int gdn_linear(const void *x, const float *x_scale, const void *w, const
 GDN_API size_t gdn_linear_bwd_workspace_size(int64_t M, int32_t N, int32_t K, int32_t act,
                                              int32_t in_dtype, int32_t dy_dtype) {
   if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype) || !act_ok(act) ||
-      !linear_sizes_ok(M, N, K, in_dtype) ||
-      M * static_cast<int64_t>(esize(in_dtype)) > kLinearMaxPitch)
+      !linear_sizes_ok(M, N, K, in_dtype))
     return 0;
   return gdn::linear_bwd_workspace_size(M, N, K, act, in_dtype, dy_dtype);
 }
@@ -1219,10 +1218,8 @@ GDN_API int gdn_linear_bwd(const void *dy, const void *pre, const void *x, const
   if (!dtype_ok(in_dtype) || !dtype_ok(dy_dtype))
     return fail(GDN_ERR_UNSUPPORTED, "%s", "dtypes must be GDN_F32, GDN_BF16 or GDN_F16");
   if (!act_ok(act)) return fail(GDN_ERR_UNSUPPORTED, "%s", "unknown activation");
-  if (!linear_sizes_ok(M, N, K, in_dtype) ||
-      M * static_cast<int64_t>(esize(in_dtype)) > kLinearMaxPitch)
-    return fail(GDN_ERR_INVALID_ARG, "%s",
-                "M must be >= 0, N and K > 0, and rows and columns at most 8 MiB");
+  if (!linear_sizes_ok(M, N, K, in_dtype))
+    return fail(GDN_ERR_INVALID_ARG, "%s", "M must be >= 0, N and K > 0, and rows at most 8 MiB");
   if (M > 0 && !dy) return fail(GDN_ERR_INVALID_ARG, "%s", "dy is required");
   if (M > 0 && act != GDN_ACT_NONE && !pre)
     return fail(GDN_ERR_INVALID_ARG, "%s", "an activation needs pre");

@@ -4,11 +4,11 @@
 //     u = x w^T + bias        y = act(u) + residual
 //     du = dy act'(u)         dx = du w     dw = du^T x     dbias = sum over rows of du
 //
-// Every product is the same kernel: C[m][n] = sum_r P[m][r] Q[n][r], both
-// operands with the reduction index r contiguous, rows a whole number of
-// 16-byte vectors apart. Operands that are not laid out so (odd widths, the
-// transposes that the backward reduces over) are first copied into the
-// workspace, padded with zeros.
+// Every product is one form: C[m][n] = sum_r P[m][r] Q[n][r], each operand in
+// memory either by its rows (r contiguous, as x and w in the forward) or by the
+// reduction axis (m or n contiguous, as w, x and du in the backward), with rows
+// a whole number of 16-byte vectors apart. Operands of other widths are first
+// copied into the workspace, padded with zeros.
 #include <type_traits>
 
 #include "gdn_device.h"
@@ -269,7 +269,8 @@ struct GemmArgs {
   int64_t ldp, ldq;          // bytes between rows, multiples of 16
   int64_t M;
   int N;
-  int rbytes;                // bytes of the reduction axis, a multiple of 16
+  int64_t rbytes;            // bytes of the reduction axis (by rows: with padding, whole vectors)
+  int64_t red;               // its indices
   int steps;                 // kStep-byte steps per split
   float *part;               // null: epilogue; else [splits][M][ldpart] sums
   int64_t ldpart;
@@ -278,11 +279,128 @@ struct GemmArgs {
   Epilogue e;
 };
 
+// One operand of a tile: TILE rows (outputs) by a stage of 128 bytes of the
+// reduction axis (64 16-bit or 32 fp32 indices), loaded straight to LDS by four
+// waves, 1 KiB an instruction: lane L's 16 bytes land at byte 16 L. What lane L
+// fetches is permuted so that the fragment reads touch all banks evenly.
+//
+// BYRED false: rows of 128 bytes, 8 an instruction; vector v of row r lies at
+// v ^ (r % 8). BYRED true: reduction index k is a row of TILE elements; its
+// 16-bit elements lie with 32-byte group u at u ^ (k % 4 + 4 (k / 8 % 2)), fp32
+// ones with 64-byte group u at u ^ (k / 4 % 4).
+//
+// A lane's fragment of output row c (lane % 16 of a group of 16) holds, as
+// vector `part` (0 or 1), the reduction bytes 64 part + 16 (lane / 16) .. + 15
+// of the stage. By rows that is one 16-byte read; by the reduction axis, 16-bit
+// elements come through the transposing LDS read, 4 indices of 16 outputs at a
+// time, and fp32 ones one by one.
+template <typename T, int TILE, bool BYRED>
+struct Operand {
+  static constexpr int ES = sizeof(T);
+  static constexpr int BYTES = TILE * kStep;
+  static constexpr int LOADS = TILE / 32;            // per wave and stage
+  static constexpr int RB = BYRED ? TILE * ES : kStep;  // bytes of a row in LDS
+  static constexpr int VPR = RB / 16;                // vectors of a row
+  static constexpr int INDICES = kStep / ES;         // reduction indices of a stage
+  static constexpr int GROUPS = TILE == 256 ? 8 : 4;  // 16-row groups of a wave
+
+  i32x4 rsrc;
+  const char *base;
+  int64_t ld, bytes;        // BYRED: pitch, bytes from base to the operand's end
+  uint32_t off[LOADS];
+  uint32_t vec, r;
+  int rbytes;
+  uint32_t at;              // LDS byte of the operand in stage 0
+  uint32_t frag[BYRED && ES == 2 ? GROUPS : 1];
+  uint32_t wbase;
+
+  // rows [o0, o0 + TILE) of `outs`; w0: the wave's first row of the tile
+  __device__ __forceinline__ void init(const char *p, int64_t pitch, int64_t o0, int64_t outs,
+                                       int64_t red_bytes, int64_t red, uint32_t lds, int lane,
+                                       int wave, int w0) {
+    const int lc = lane % 16, lg = lane / 16;
+    at = lds;
+    ld = pitch;
+    if constexpr (BYRED) {
+      base = p + o0 * ES;
+      bytes = red * pitch - o0 * ES;
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int at16 = (wave + 4 * i) * 64 + lane, k = at16 / VPR, v = at16 % VPR;
+        const int x = ES == 2 ? 2 * (k % 4 + 4 * (k / 8 % 2)) : 4 * (k / 4 % 4);
+        off[i] = static_cast<uint32_t>(k * pitch + (v ^ x) * 16);
+      }
+      if constexpr (ES == 2) {
+        const int f = lc / 4 + 4 * (lg & 1);
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q)
+          frag[q] = (8 * lg + lc / 4) * RB + ((w0 / 16 + q) ^ f) * 32 + (lc % 4 / 2) * 16 +
+                    (lc & 1) * 8;
+      } else {
+        frag[0] = 4 * lg * RB + lc * 4;
+        wbase = w0 / 16;
+      }
+    } else {
+      // rows past the operand's end lie past the resource's end and read as zeros
+      const int64_t rows = outs - o0 < TILE ? outs - o0 : TILE;
+      rsrc = buffer_rsrc(p + o0 * pitch, static_cast<uint32_t>(rows * pitch));
+      vec = ((lane % 8) ^ (lane / 8)) * 16;
+      rbytes = static_cast<int>(red_bytes);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        off[i] = static_cast<uint32_t>(((wave + 4 * i) * 8 + lane / 8) * pitch);
+      frag[0] = lc * 128 + ((lg ^ (lc & 7)) * 16);
+      wbase = w0 * 128;
+    }
+  }
+  // stage s is loaded next; `valid` false: zeros. So are bytes past the axis.
+  __device__ __forceinline__ void stage(int s, bool valid) {
+    if constexpr (BYRED) {
+      const int64_t skip = static_cast<int64_t>(s) * INDICES * ld;
+      const int64_t left = valid ? bytes - skip : 0;
+      rsrc = buffer_rsrc(base + skip, static_cast<uint32_t>(
+                                          left < 0 ? 0 : left < 0x40000000 ? left : 0x40000000));
+    } else {
+      r = s * kStep + vec;
+      if (!valid || static_cast<int>(r) >= rbytes) r = 0x80000000u;
+    }
+  }
+  __device__ __forceinline__ void load(int i, uint32_t stage_off, int wave) {
+    dma16(rsrc, BYRED ? off[i] : off[i] + r, at + stage_off + (wave + 4 * i) * 1024);
+  }
+  // vector `part` of the fragment of the wave's row group q
+  __device__ __forceinline__ i32x4 read(const char *smem, uint32_t stage_off, int q,
+                                        int part) const {
+    const char *from = smem + (at - lds_addr(smem)) + stage_off;
+    if constexpr (!BYRED) {
+      return *reinterpret_cast<const i32x4 *>(from + wbase + 16 * q * 128 + (frag[0] ^ (64 * part)));
+    } else if constexpr (ES == 2) {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s16x4 lds4;
+      struct Two {
+        s16x4 v[2];
+      } two;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        two.v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4 *)(from + frag[q] + (32 * part + 4 * h) * RB));
+      return __builtin_bit_cast(i32x4, two);
+    } else {
+      i32x4 x;
+      const int lg = threadIdx.x % 64 / 16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = *reinterpret_cast<const int32_t *>(from + frag[0] + (16 * part + e) * RB +
+                                                  ((wbase + q) ^ lg) * 64);
+      return x;
+    }
+  }
+};
+
 // One kTile x kTile tile of C (times one split of the reduction) per workgroup
-// of four waves, each 64 x 64 of it in 16 x 16 accumulators. A stage holds
-// 128 bytes of the reduction axis of every operand row, loaded straight to
-// LDS; the next stage is in flight while one is multiplied.
-template <typename T, bool EXACT>
+// of four waves, each 64 x 64 of it in 16 x 16 accumulators; the next stage is
+// in flight while one is multiplied.
+template <typename T, bool EXACT, bool PRED, bool QRED>
 __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
   constexpr int STAGE = 2 * kTile * kStep;
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
@@ -294,31 +412,20 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
   const int n0 = at.n * kTile;
   const int wm = (wave / 2) * 64, wn = (wave % 2) * 64;
 
-  // rows past the operand's end lie past the resource's end and read as zeros
-  const int64_t mrows = g.M - m0 < kTile ? g.M - m0 : kTile;
-  const int nrows = g.N - n0 < kTile ? g.N - n0 : kTile;
-  const i32x4 rp = buffer_rsrc(g.p + m0 * g.ldp, static_cast<uint32_t>(mrows * g.ldp));
-  const i32x4 rq = buffer_rsrc(g.q + n0 * g.ldq, static_cast<uint32_t>(nrows * g.ldq));
-
-  // A load instruction covers 8 rows of 128 bytes; lane L lands at byte 16 L
-  // of its 1 KiB, row L / 8, vector L % 8. It fetches vector (L % 8) ^ (row % 8)
-  // of its row, so that the fragment reads below touch all banks evenly.
-  const int row = lane / 8;
-  const int vecoff = ((lane % 8) ^ row) * 16;
+  Operand<T, kTile, PRED> P;
+  Operand<T, kTile, QRED> Q;
+  P.init(g.p, g.ldp, m0, g.M, g.rbytes, g.red, lds_addr(smem), lane, wave, wm);
+  Q.init(g.q, g.ldq, n0, g.N, g.rbytes, g.red, lds_addr(smem) + kTile * kStep, lane, wave, wn);
   const int s0 = blockIdx.y * g.steps;
-  const int total = (g.rbytes + kStep - 1) / kStep;
+  const int total = static_cast<int>((g.rbytes + kStep - 1) / kStep);
   const int s1 = s0 + g.steps < total ? s0 + g.steps : total;
   auto issue = [&](int s, int buf) {
-    const int r = s * kStep + vecoff;
-    const bool in = r < g.rbytes;
-    const uint32_t base = lds_addr(smem) + buf * STAGE;
+    P.stage(s, true);
+    Q.stage(s, true);
 #pragma unroll
     for (int i = 0; i < kTile / 32; ++i) {
-      const int blk = wave + 4 * i;
-      const uint32_t op = static_cast<uint32_t>((blk * 8 + row) * g.ldp) + r;
-      const uint32_t oq = static_cast<uint32_t>((blk * 8 + row) * g.ldq) + r;
-      dma16(rp, in ? op : 0x80000000u, base + blk * 1024);
-      dma16(rq, in ? oq : 0x80000000u, base + kTile * kStep + blk * 1024);
+      P.load(i, buf * STAGE, wave);
+      Q.load(i, buf * STAGE, wave);
     }
   };
 
@@ -334,16 +441,13 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
     wait_vmcnt<0>();
     wg_barrier();
     if (s + 1 < s1) issue(s + 1, buf ^ 1);
-    const char *base = smem + buf * STAGE;
-    const int o0 = lc * 128 + ((lg ^ (lc & 7)) * 16);
     u32x4 a[4][2], b[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int o = o0 ^ (64 * h);
-        a[i][h] = *reinterpret_cast<const u32x4 *>(base + kTile * kStep + (wn + 16 * i) * 128 + o);
-        b[i][h] = *reinterpret_cast<const u32x4 *>(base + (wm + 16 * i) * 128 + o);
+        a[i][h] = __builtin_bit_cast(u32x4, Q.read(smem, buf * STAGE, i, h));
+        b[i][h] = __builtin_bit_cast(u32x4, P.read(smem, buf * STAGE, i, h));
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -491,7 +595,7 @@ struct Half {
   i32x8 v[4];
 };
 
-template <typename T>
+template <typename T, bool PRED, bool QRED>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void
 gemm256_kernel(const GemmArgs g) {
   constexpr int TILE = 256, STAGE = 2 * TILE * kStep, LDC = TILE + 4;
@@ -506,48 +610,35 @@ gemm256_kernel(const GemmArgs g) {
   const int n0 = at.n * TILE;
   const int wm = (wave / 2) * 128, wn = (wave % 2) * 128;
 
-  const int64_t mrows = g.M - m0 < TILE ? g.M - m0 : TILE;
-  const int nrows = g.N - n0 < TILE ? g.N - n0 : TILE;
-  const i32x4 rp = buffer_rsrc(g.p + m0 * g.ldp, static_cast<uint32_t>(mrows * g.ldp));
-  const i32x4 rq = buffer_rsrc(g.q + n0 * g.ldq, static_cast<uint32_t>(nrows * g.ldq));
-
-  const int row = lane / 8;
-  const int vecoff = ((lane % 8) ^ row) * 16;
-  const int s0 = blockIdx.y * g.steps;
-  const int total = (g.rbytes + kStep - 1) / kStep;
-  const int s1 = s0 + g.steps < total ? s0 + g.steps : total;
-  uint32_t op[8], oq[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    op[i] = static_cast<uint32_t>(((wave + 4 * i) * 8 + row) * g.ldp);
-    oq[i] = static_cast<uint32_t>(((wave + 4 * i) * 8 + row) * g.ldq);
-  }
   const uint32_t lds0 = lds_addr(smem);
-  // load i (0..7: p, 8..15: q) of step s; past the split or the axis it reads zeros
-  auto offset = [&](int s) {
-    const int r = s * kStep + vecoff;
-    return s < s1 && r < g.rbytes ? static_cast<uint32_t>(r) : 0x80000000u;
+  Operand<T, TILE, PRED> OP;
+  Operand<T, TILE, QRED> OQ;
+  OP.init(g.p, g.ldp, m0, g.M, g.rbytes, g.red, lds0, lane, wave, wm);
+  OQ.init(g.q, g.ldq, n0, g.N, g.rbytes, g.red, lds0 + TILE * kStep, lane, wave, wn);
+  const int s0 = blockIdx.y * g.steps;
+  const int total = static_cast<int>((g.rbytes + kStep - 1) / kStep);
+  const int s1 = s0 + g.steps < total ? s0 + g.steps : total;
+  // load i (0..7: p, 8..15: q) of the stage set by next(); past the split zeros
+  auto next = [&](int s) {
+    OP.stage(s, s < s1);
+    OQ.stage(s, s < s1);
   };
-  auto load = [&](uint32_t r, int buf, int i) {
-    const uint32_t at = lds0 + buf * STAGE + (i < 8 ? 0 : TILE * kStep) + (wave + 4 * (i % 8)) * 1024;
-    if (i < 8) dma16(rp, op[i] + r, at);
-    else dma16(rq, oq[i - 8] + r, at);
+  auto load = [&](int buf, int i) {
+    if (i < 8) OP.load(i, buf * STAGE, wave);
+    else OQ.load(i - 8, buf * STAGE, wave);
   };
 
-  const int o0 = lc * 128 + ((lg ^ (lc & 7)) * 16);
   // 16 bytes of one half's fragments: vector i % 2 of row group i / 2, i = 0..7
-  auto read = [&](Half &f, int at, int i) {
-    const i32x4 x = *reinterpret_cast<const i32x4 *>(smem + at + 16 * (i / 2) * 128 +
-                                                     (o0 ^ (64 * (i % 2))));
+  auto put = [&](Half &f, const i32x4 &x, int i) {
     i32x8 &d = f.v[i / 2];
 #pragma unroll
     for (int e = 0; e < 4; ++e) d[4 * (i % 2) + e] = x[e];
   };
   auto read_a = [&](Half &f, int buf, int h, int i) {
-    read(f, buf * STAGE + TILE * kStep + (wn + 64 * h) * 128, i);
+    put(f, OQ.read(smem, buf * STAGE, 4 * h + i / 2, i % 2), i);
   };
   auto read_b = [&](Half &f, int buf, int h, int i) {
-    read(f, buf * STAGE + (wm + 64 * h) * 128, i);
+    put(f, OP.read(smem, buf * STAGE, 4 * h + i / 2, i % 2), i);
   };
 
   f32x4 acc[8][8];  // [n tile][m tile]
@@ -579,23 +670,24 @@ gemm256_kernel(const GemmArgs g) {
     quadrant(A0, Bs, 0, 1 - P, [&](int i) { read_a(A1, P, 1, i); });
     wait_vmcnt<0>();
     wg_barrier();
-    const uint32_t r = offset(s + 2);
+    next(s + 2);
     quadrant(A1, Bs, 1, 1 - P, [&](int i) {
       read_a(A0, 1 - P, 0, i);
-      load(r, P, i);
+      load(P, i);
     });
     quadrant(A1, Bf, 1, P, [&](int i) {
       read_b(Bs, 1 - P, 1 - P, i);
-      load(r, P, 8 + i);
+      load(P, 8 + i);
     });
   };
 
   if (s0 < s1) {
-    const uint32_t r0 = offset(s0), r1 = offset(s0 + 1);
+    next(s0);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) load(r0, 0, i);
+    for (int i = 0; i < 16; ++i) load(0, i);
+    next(s0 + 1);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) load(r1, 1, i);
+    for (int i = 0; i < 16; ++i) load(1, i);
     wait_vmcnt<16>();
     wg_barrier();
 #pragma unroll
@@ -678,50 +770,50 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const E *__restrict__ src
   }
 }
 
-// dst[c][0 .. pitch) = src[0 .. rows)[c] and zeros, by 64 x 64 tiles
-template <typename E>
-__global__ __launch_bounds__(256) void transpose_kernel(const E *__restrict__ src, int64_t rows,
-                                                        int cols, int64_t ld, E *__restrict__ dst,
-                                                        int64_t pitch) {
-  __shared__ E s[64][65];
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int c0 = blockIdx.y * 64;
-  const int lo = threadIdx.x % 64, hi = threadIdx.x / 64;
-  for (int i = hi; i < 64; i += 4)
-    s[i][lo] = r0 + i < rows && c0 + lo < cols ? src[(r0 + i) * ld + c0 + lo] : E(0);
-  __syncthreads();
-  for (int i = hi; i < 64; i += 4)
-    if (c0 + i < cols && r0 + lo < pitch) dst[(c0 + i) * pitch + r0 + lo] = s[lo][i];
-}
-
 // du[m][0 .. pitch) = dy act'(pre), zeros from N on (du may be null), and the
-// column sums of du over each run of `run` rows (part may be null). A
-// workgroup owns 64 columns of one run.
+// column sums of the unrounded du over each run of `run` rows (part may be
+// null). A workgroup owns 256 columns of one run: 8 columns of every eighth row
+// a thread. `vec`: N is a multiple of 8, so that the groups are whole vectors.
 template <typename TG, typename T>
 __global__ __launch_bounds__(256) void du_kernel(const TG *__restrict__ dy,
                                                  const TG *__restrict__ pre, int64_t M, int N,
                                                  int act, T *__restrict__ du, int pitch, int run,
                                                  float *__restrict__ part) {
-  __shared__ float s[4][64];
-  const int lo = threadIdx.x % 64, hi = threadIdx.x / 64;
-  const int n = blockIdx.x * 64 + lo;
+  __shared__ float s[8][257];
+  const bool vec = N % 8 == 0;
+  const int g = threadIdx.x % 32, hi = threadIdx.x / 32;
+  const int n = blockIdx.x * 256 + 8 * g;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * run;
   const int64_t m1 = m0 + run < M ? m0 + run : M;
-  float sum = 0.0f;
-  for (int64_t m = m0 + hi; m < m1; m += 4) {
-    float v = 0.0f;
-    if (n < N) {
-      v = io<TG>::to_f32(dy[m * N + n]);
-      if (act) v *= act_slope(io<TG>::to_f32(pre[m * N + n]), act);
+  float sum[8] = {};
+#pragma unroll 2
+  for (int64_t m = m0 + hi; m < m1; m += 8) {
+    float v[8];
+    load8(dy + m * N, n, N, vec, v);
+    if (act) {
+      float u[8];
+      load8(pre + m * N, n, N, vec, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= act_slope(u[i], act);
     }
-    sum += v;
-    if (du && n < pitch) du[m * pitch + n] = io<T>::from_f32(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    if (du) {
+      // v is zero from N on (whatever act_slope gives there meets a zero dy)
+      store8(du + m * pitch, n, pitch, vec, v);
+    }
   }
   if (!part) return;
-  s[hi][lo] = sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[hi][8 * g + i] = sum[i];
   __syncthreads();
-  if (hi == 0 && n < N)
-    part[static_cast<size_t>(blockIdx.y) * N + n] = ((s[0][lo] + s[1][lo]) + s[2][lo]) + s[3][lo];
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col < N) {
+    float t = s[0][threadIdx.x];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) t += s[q][threadIdx.x];
+    part[static_cast<size_t>(blockIdx.y) * N + col] = t;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -774,43 +866,59 @@ GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes, bool large) {
 // instructions (fp32 sums of 8-bit operands are taken by the small one)
 bool large_ok(int dtype, int out_dtype) { return dtype != 0 && !(dtype == kE4m3 && out_dtype == 0); }
 
-hipError_t run_gemm(const void *P, int64_t ldp, const void *Q, int64_t ldq, int64_t M, int N,
-                    int64_t rbytes, int dtype, const Epilogue &e, char *part, hipStream_t stream) {
+struct Matrix {
+  const void *p;
+  int64_t ld;   // bytes
+  bool by_red;  // the reduction axis is the slow one
+};
+
+template <typename T, bool EXACT, bool PRED, bool QRED>
+hipError_t start_gemm(const GemmArgs &g, const GemmPlan &p, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.tiles_m * p.tiles_n), p.splits);
+  if constexpr (!__is_same(T, float) && (!__is_same(T, e4m3_t) || !EXACT)) {
+    if (p.tile == 256) {
+      hipLaunchKernelGGL((gemm256_kernel<T, PRED, QRED>), grid, dim3(256), 0, stream, g);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((gemm_kernel<T, EXACT, PRED, QRED>), grid, dim3(256), 0, stream, g);
+  return hipGetLastError();
+}
+
+// C = P Q^T through the epilogue: M by N outputs, `red` reduction indices, that
+// operands by rows hold padded with zeros to `pitch` of them
+hipError_t run_gemm(const Matrix &P, const Matrix &Q, int64_t M, int N, int64_t pitch, int64_t red,
+                    int dtype, const Epilogue &e, char *part, hipStream_t stream) {
   if (M == 0) return hipSuccess;
+  const int64_t rbytes = pitch * esize(dtype);
   const GemmPlan p = plan_gemm(M, N, rbytes, large_ok(dtype, e.out_dtype));
   GemmArgs g;
-  g.p = static_cast<const char *>(P);
-  g.q = static_cast<const char *>(Q);
-  g.ldp = ldp;
-  g.ldq = ldq;
+  g.p = static_cast<const char *>(P.p);
+  g.q = static_cast<const char *>(Q.p);
+  g.ldp = P.ld;
+  g.ldq = Q.ld;
   g.M = M;
   g.N = N;
-  g.rbytes = static_cast<int>(rbytes);
+  g.rbytes = rbytes;
+  g.red = red;
   g.steps = p.steps;
   g.part = p.splits > 1 ? reinterpret_cast<float *>(part) : nullptr;
   g.ldpart = p.ldpart;
   g.tiles_m = p.tiles_m;
   g.tiles_n = p.tiles_n;
   g.e = e;
-  const dim3 grid(static_cast<unsigned>(p.tiles_m * p.tiles_n), p.splits);
-  if (p.tile == 256) {
-    if (dtype == kE4m3)
-      hipLaunchKernelGGL(gemm256_kernel<e4m3_t>, grid, dim3(256), 0, stream, g);
-    else if (dtype == 1)
-      hipLaunchKernelGGL(gemm256_kernel<bf16_t>, grid, dim3(256), 0, stream, g);
-    else
-      hipLaunchKernelGGL(gemm256_kernel<_Float16>, grid, dim3(256), 0, stream, g);
-  } else if (dtype == kE4m3 && e.out_dtype == 0)
-    hipLaunchKernelGGL((gemm_kernel<e4m3_t, true>), grid, dim3(256), 0, stream, g);
-  else if (dtype == kE4m3)
-    hipLaunchKernelGGL((gemm_kernel<e4m3_t, false>), grid, dim3(256), 0, stream, g);
-  else if (dtype == 1)
-    hipLaunchKernelGGL((gemm_kernel<bf16_t, true>), grid, dim3(256), 0, stream, g);
-  else if (dtype == 2)
-    hipLaunchKernelGGL((gemm_kernel<_Float16, true>), grid, dim3(256), 0, stream, g);
-  else
-    hipLaunchKernelGGL((gemm_kernel<float, true>), grid, dim3(256), 0, stream, g);
-  hipError_t err = hipGetLastError();
+  hipError_t err;
+  if (dtype == kE4m3) {
+    err = e.out_dtype == 0 ? start_gemm<e4m3_t, true, false, false>(g, p, stream)
+                           : start_gemm<e4m3_t, false, false, false>(g, p, stream);
+  } else {
+    err = with_type(dtype, [&](auto t) {
+      using T = decltype(t);
+      if (P.by_red) return start_gemm<T, true, true, true>(g, p, stream);
+      if (Q.by_red) return start_gemm<T, true, false, true>(g, p, stream);
+      return start_gemm<T, true, false, false>(g, p, stream);
+    });
+  }
   if (err != hipSuccess || !g.part) return err;
   const int64_t quads = M * (p.ldpart / 4);
   hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0,
@@ -833,17 +941,6 @@ hipError_t pad_rows(const void *src, int64_t rows, int cols, void *dst, int pitc
     hipLaunchKernelGGL(pad_rows_kernel<E>, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)),
                        dim3(256), 0, stream, static_cast<const E *>(src), rows, cols,
                        static_cast<E *>(dst), pitch);
-  });
-  return hipGetLastError();
-}
-
-hipError_t transpose(const void *src, int64_t rows, int cols, int64_t ld, void *dst, int64_t pitch,
-                     int es, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((pitch + 63) / 64), (cols + 63) / 64);
-  by_size(es, [&](auto e) {
-    using E = decltype(e);
-    hipLaunchKernelGGL(transpose_kernel<E>, grid, dim3(256), 0, stream,
-                       static_cast<const E *>(src), rows, cols, ld, static_cast<E *>(dst), pitch);
   });
   return hipGetLastError();
 }
@@ -880,34 +977,36 @@ int du_run(int64_t M) {
   return static_cast<int>(r < 64 ? 64 : r);
 }
 
-// backward workspace: du (when it is not dy itself), the transposes of w, du
-// and x, partial sums of dbias, partial sums of one product at a time
+// backward workspace: du (when it is not dy itself), padded copies of x and w
+// where K is no whole vector, partial sums of dbias, partial sums of one
+// product at a time
 struct BwdLayoutL {
-  bool own_du;
-  int64_t pn, pm;  // pitches of du and w^T (over N), of du^T and x^T (over M)
-  size_t du, wt, dut, xt, db, part, total;
+  bool own_du, pad;
+  int64_t pn, pk;  // elements between rows of du, and of x and w
+  size_t du, x, w, db, part, total;
 };
 BwdLayoutL bwd_layout(int64_t M, int N, int K, int act, int in_dtype, int dy_dtype) {
   const int es = esize(in_dtype);
   BwdLayoutL L;
-  const int64_t rn = round16(static_cast<int64_t>(N) * es), rm = round16(M * es);
+  const int64_t rn = round16(static_cast<int64_t>(N) * es);
+  const int64_t rk = round16(static_cast<int64_t>(K) * es);
   L.pn = rn / es;
-  L.pm = rm / es;
+  L.pk = rk / es;
   L.own_du = act != 0 || dy_dtype != in_dtype || L.pn != N;
+  L.pad = L.pk != K;
   size_t off = 0;
   L.du = off;
   if (L.own_du) off += align256(static_cast<size_t>(M) * rn);
-  L.wt = off;
-  off += align256(static_cast<size_t>(K) * rn);
-  L.dut = off;
-  off += align256(static_cast<size_t>(N) * rm);
-  L.xt = off;
-  off += align256(static_cast<size_t>(K) * rm);
+  L.x = off;
+  if (L.pad) off += align256(static_cast<size_t>(M) * rk);
+  L.w = off;
+  if (L.pad) off += align256(static_cast<size_t>(N) * rk);
   L.db = off;
   off += align256(static_cast<size_t>((M + du_run(M) - 1) / du_run(M)) * N * 4);
   L.part = off;
-  const size_t p1 = plan_gemm(M, K, rn, large_ok(in_dtype, in_dtype)).part_bytes;
-  const size_t p2 = plan_gemm(N, K, rm, large_ok(in_dtype, in_dtype)).part_bytes;
+  const bool large = large_ok(in_dtype, in_dtype);
+  const size_t p1 = plan_gemm(M, K, rn, large).part_bytes;
+  const size_t p2 = plan_gemm(N, K, M * es, large).part_bytes;
   off += p1 > p2 ? p1 : p2;
   L.total = off;
   return L;
@@ -934,8 +1033,8 @@ hipError_t launch_linear(const LinearArgs &a) {
   }
   const Epilogue e{a.x_scale, a.w_scale, a.bias, a.residual, a.pre, a.y, a.M, a.N, a.act,
                    a.out_dtype};
-  return run_gemm(x, L.pitch * es, w, L.pitch * es, a.M, a.N, L.pitch * es, a.in_dtype, e,
-                  a.ws + L.part, a.stream);
+  return run_gemm({x, L.pitch * es, false}, {w, L.pitch * es, false}, a.M, a.N, L.pitch,
+                  a.K, a.in_dtype, e, a.ws + L.part, a.stream);
 }
 
 size_t linear_bwd_workspace_size(int64_t M, int N, int K, int act, int in_dtype, int dy_dtype) {
@@ -955,7 +1054,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a) {
       return with_type(a.dy_dtype, [&](auto tg) {
         using T = decltype(t);
         using TG = decltype(tg);
-        hipLaunchKernelGGL((du_kernel<TG, T>), dim3(static_cast<unsigned>((L.pn + 63) / 64), runs),
+        hipLaunchKernelGGL((du_kernel<TG, T>), dim3(static_cast<unsigned>((L.pn + 255) / 256), runs),
                            dim3(256), 0, a.stream, static_cast<const TG *>(a.dy),
                            static_cast<const TG *>(a.pre), a.M, a.N, a.act,
                            L.own_du ? reinterpret_cast<T *>(a.ws + L.du) : nullptr,
@@ -969,29 +1068,35 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a) {
     err = launch_colsum(db, runs, a.N, a.dbias, a.stream);
     if (err != hipSuccess) return err;
   }
+  const int64_t ldn = L.pn * es, ldk = L.pk * es;
   Epilogue e{};
   e.N = a.K;
   e.out_dtype = a.in_dtype;
   if (a.dx && a.M > 0) {
-    err = transpose(a.w, a.N, a.K, a.K, a.ws + L.wt, L.pn, es, a.stream);
-    if (err != hipSuccess) return err;
+    const void *w = a.w;
+    if (L.pad) {
+      err = pad_rows(a.w, a.N, a.K, a.ws + L.w, static_cast<int>(L.pk), es, a.stream);
+      if (err != hipSuccess) return err;
+      w = a.ws + L.w;
+    }
     e.M = a.M;
     e.y = a.dx;
-    err = run_gemm(du, L.pn * es, a.ws + L.wt, L.pn * es, a.M, a.K, L.pn * es, a.in_dtype, e,
+    // the reduction stops at N: past it du has zeros, but w no rows
+    err = run_gemm({du, ldn, false}, {w, ldk, true}, a.M, a.K, L.pn, a.N, a.in_dtype, e,
                    a.ws + L.part, a.stream);
     if (err != hipSuccess) return err;
   }
   if (a.dw) {
-    if (a.M > 0) {
-      err = transpose(du, a.M, a.N, L.pn, a.ws + L.dut, L.pm, es, a.stream);
+    const void *x = a.x;
+    if (L.pad && a.M > 0) {
+      err = pad_rows(a.x, a.M, a.K, a.ws + L.x, static_cast<int>(L.pk), es, a.stream);
       if (err != hipSuccess) return err;
-      err = transpose(a.x, a.M, a.K, a.K, a.ws + L.xt, L.pm, es, a.stream);
-      if (err != hipSuccess) return err;
+      x = a.ws + L.x;
     }
     e.M = a.N;
     e.y = a.dw;
-    err = run_gemm(a.ws + L.dut, L.pm * es, a.ws + L.xt, L.pm * es, a.N, a.K, L.pm * es,
-                   a.in_dtype, e, a.ws + L.part, a.stream);
+    err = run_gemm({du, ldn, true}, {x, ldk, true}, a.N, a.K, a.M, a.M, a.in_dtype, e,
+                   a.ws + L.part, a.stream);
   }
   return err;
 }

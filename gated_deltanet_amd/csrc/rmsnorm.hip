@@ -27,59 +27,6 @@ constexpr float kE4m3Max = 448.0f;  // largest finite e4m3 value
 // their maximum: the scale stays a normal number and its reciprocal finite.
 constexpr float kTinyMax = 1e-30f;
 
-// Elements e0 .. e0 + 7 of a row of d, zeros past the end. `vec`: d is a
-// multiple of 8, so that every group is whole and 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int e0, int d, bool vec, float *o) {
-  if (vec) {
-    if (e0 < d) {
-      Vec8<T>::load(row + e0, o);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = e0 + i < d ? io<T>::to_f32(row[e0 + i]) : 0.0f;
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T *row, int e0, int d, bool vec, const float *v) {
-  if (vec) {
-    if (e0 < d) Vec8<T>::store(row + e0, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (e0 + i < d) row[e0 + i] = io<T>::from_f32(v[i]);
-  }
-}
-
-// e4m3 bytes of eight values already divided by the row's scale. |v| is at
-// most 448 (1 + 2^-22), which rounds to 448: the conversion cannot overflow.
-__device__ __forceinline__ u32x2 to_e4m3(const float *v) {
-  u32x2 r;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h], v[4 * h + 1], 0, false);
-    r[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], p, true);
-  }
-  return r;
-}
-
-template <>
-__device__ __forceinline__ void store8<e4m3_t>(e4m3_t *row, int e0, int d, bool vec,
-                                               const float *v) {
-  const u32x2 q = to_e4m3(v);
-  if (vec) {
-    if (e0 < d) *reinterpret_cast<u32x2 *>(row + e0) = q;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (e0 + i < d) row[e0 + i].bits = static_cast<uint8_t>(q[i / 4] >> (8 * (i % 4)));
-  }
-}
-
 // the larger of two values, NaN if either is (a NaN in a row reaches its scale)
 __device__ __forceinline__ float max_nan(float m, float v) { return (v > m || v != v) ? v : m; }
 

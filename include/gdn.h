@@ -634,11 +634,12 @@ GDN_API int gdn_linear(const void *x, const float *x_scale, const void *w,
  *            NULL to skip it. With M = 0, dw and dbias are zeros.
  *   workspace  device memory, 256-byte aligned, of at least
  *            gdn_linear_bwd_workspace_size(M, N, K, act, in_dtype, dy_dtype)
- *            bytes, overwritten: du where it differs from dy, operands laid
- *            out for the products, partial sums.
+ *            bytes, overwritten: du where it differs from dy, padded copies
+ *            of x and w where a row of K elements is no whole number of
+ *            16-byte vectors, partial sums.
  * The products take du rounded to in_dtype (as the matrix cores need it) and
- * sum in fp32; dbias sums the unrounded du. Sizes as gdn_linear, and a column
- * of M elements is at most 8 MiB. Sums are added in a fixed order.
+ * sum in fp32; dbias sums the unrounded du. Sizes as gdn_linear. Sums are
+ * added in a fixed order.
  */
 GDN_API size_t gdn_linear_bwd_workspace_size(int64_t M, int32_t N, int32_t K,
                                              int32_t act, int32_t in_dtype,

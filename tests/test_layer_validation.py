@@ -118,7 +118,7 @@ BWD = dict(dy=X, pre=P, x=R, w=W, dx=O, dw=Y, db=S, M=100, N=64, K=128, act=1, i
 @pytest.mark.parametrize("kw,code", [
     (dict(dy=None), INVALID), (dict(pre=None), INVALID), (dict(x=None), INVALID),
     (dict(w=None), INVALID), (dict(it=E4M3), UNSUPPORTED), (dict(gt=E4M3), UNSUPPORTED),
-    (dict(act=9), UNSUPPORTED), (dict(M=(1 << 22) + 8), INVALID), (dict(N=0), INVALID),
+    (dict(act=9), UNSUPPORTED), (dict(M=1 << 31), INVALID), (dict(N=0), INVALID),
     (dict(dx=O + 8), MISALIGNED), (dict(dw=Y + 8), MISALIGNED), (dict(db=S + 2), MISALIGNED),
     (dict(dx=X), INVALID), (dict(dw=W), INVALID), (dict(db=Y), INVALID), (dict(dw=O), INVALID),
     (dict(ws=None), INVALID), (dict(wb=256), INVALID), (dict(ws=WS + 32), MISALIGNED),
