@@ -888,8 +888,20 @@ def gdn_chunk_fwd_fused(q_raw, k_raw, v_raw, conv_w, log_alpha, beta, z, S0=None
     return o, S_T
 
 
+_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float16: GDN_F16}
+
+
+def _code(t: torch.dtype) -> int:
+    return _CODES[t] if t in _CODES else _dt(t)
+
+
 def _dt8(t: torch.dtype) -> int:
-    return GDN_E4M3 if t == torch.float8_e4m3fn else _dt(t)
+    return GDN_E4M3 if t == torch.float8_e4m3fn else _code(t)
+
+
+def _ptr(t):
+    """Address of an optional tensor, as a c_void_p argument takes it."""
+    return None if t is None else t.data_ptr()
 
 
 def _rows_d(x, name):
@@ -927,11 +939,13 @@ def _launch(lib, name, dev, *args):
     launch on the current device)."""
     fn = getattr(lib, name)
     if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream(dev))
+        # the stream's handle without a Stream object, 2 us a call cheaper
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, _stream(dev))
-    _check(rc, lib, name)
+    if rc != GDN_OK:
+        _check(rc, lib, name)
 
 
 def gdn_add_rmsnorm(x, norm_w=None, residual=None, rms_eps=1e-6, out_dtype=None, y=None, r=None,
@@ -945,7 +959,7 @@ def gdn_add_rmsnorm(x, norm_w=None, residual=None, rms_eps=1e-6, out_dtype=None,
     lib = load_library()
     _need(x, "x")
     rows, d = _rows_d(x, "x")
-    in_code = _dt(x.dtype)
+    in_code = _code(x.dtype)
     out_dtype = x.dtype if out_dtype is None else out_dtype
     out_code = _dt8(out_dtype)
     _vector(norm_w, "norm_w", d)
@@ -960,13 +974,13 @@ def gdn_add_rmsnorm(x, norm_w=None, residual=None, rms_eps=1e-6, out_dtype=None,
     dev = _devices((x, "x"), (norm_w, "norm_w"), (residual, "residual"), (y, "y"), (r, "r"),
                    (y_scale, "y_scale"))
     if y is None:
-        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        y = torch.empty_like(x, dtype=out_dtype)
     if r is None and residual is not None:
         r = torch.empty_like(x)
     if y_scale is None and out_code == GDN_E4M3:
         y_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    _launch(lib, "gdn_add_rmsnorm", dev, _p(x), _p(residual), _p(norm_w), float(rms_eps), _p(r),
-            _p(y), _p(y_scale), rows, d, in_code, out_code)
+    _launch(lib, "gdn_add_rmsnorm", dev, _ptr(x), _ptr(residual), _ptr(norm_w), float(rms_eps), _ptr(r),
+            _ptr(y), _ptr(y_scale), rows, d, in_code, out_code)
     return y, r, y_scale
 
 
@@ -976,15 +990,15 @@ def gdn_quantize_rows(x, y=None, y_scale=None):
     lib = load_library()
     _need(x, "x")
     rows, d = _rows_d(x, "x")
-    in_code = _dt(x.dtype)
+    in_code = _code(x.dtype)
     _like(y, "y", x.shape, torch.float8_e4m3fn)
     _like(y_scale, "y_scale", x.shape[:-1], torch.float32)
     dev = _devices((x, "x"), (y, "y"), (y_scale, "y_scale"))
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev)
+        y = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     if y_scale is None:
         y_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    _launch(lib, "gdn_quantize_rows", dev, _p(x), _p(y), _p(y_scale), rows, d, in_code)
+    _launch(lib, "gdn_quantize_rows", dev, _ptr(x), _ptr(y), _ptr(y_scale), rows, d, in_code)
     return y, y_scale
 
 
@@ -1002,10 +1016,10 @@ def gdn_add_rmsnorm_bwd(dy, r, norm_w=None, dr=None, rms_eps=1e-6, want_dnorm_w=
     lib = load_library()
     _need(r, "r")
     rows, d = _rows_d(r, "r")
-    in_code = _dt(r.dtype)
+    in_code = _code(r.dtype)
     _need(dy, "dy")
     _shape(dy, "dy", r.shape)
-    dy_code = _dt(dy.dtype)
+    dy_code = _code(dy.dtype)
     _vector(norm_w, "norm_w", d)
     _like(dr, "dr", r.shape, r.dtype)
     _like(dx, "dx", r.shape, r.dtype)
@@ -1022,8 +1036,8 @@ def gdn_add_rmsnorm_bwd(dy, r, norm_w=None, dr=None, rms_eps=1e-6, want_dnorm_w=
         if dnorm_w is None:
             dnorm_w = torch.empty(d, dtype=torch.float32, device=dev)
     workspace, nbytes = _workspace(workspace, need, dev)
-    _launch(lib, "gdn_add_rmsnorm_bwd", dev, _p(dy), _p(r), _p(dr), _p(norm_w), float(rms_eps),
-            _p(dx), _p(dnorm_w), rows, d, in_code, dy_code, _p(workspace), nbytes)
+    _launch(lib, "gdn_add_rmsnorm_bwd", dev, _ptr(dy), _ptr(r), _ptr(dr), _ptr(norm_w), float(rms_eps),
+            _ptr(dx), _ptr(dnorm_w), rows, d, in_code, dy_code, _ptr(workspace), nbytes)
     return dx, dnorm_w
 
 
@@ -1056,7 +1070,7 @@ def gdn_linear(x, w, bias=None, residual=None, act="none", out_dtype=None, x_sca
     N = w.shape[0]
     if out_dtype is None:
         out_dtype = torch.bfloat16 if in_code == GDN_E4M3 else x.dtype
-    out_code = _dt(out_dtype)
+    out_code = _code(out_dtype)
     act_code = _act_code(act)
     if (in_code == GDN_E4M3) != (x_scale is not None) or (x_scale is None) != (w_scale is None):
         raise GdnError("x_scale and w_scale go with e4m3 inputs")
@@ -1076,8 +1090,8 @@ def gdn_linear(x, w, bias=None, residual=None, act="none", out_dtype=None, x_sca
     if pre is None and want_pre:
         pre = torch.empty(shape, dtype=out_dtype, device=dev)
     workspace, nbytes = _workspace(workspace, lib.gdn_linear_workspace_size(M, N, K, in_code), dev)
-    _launch(lib, "gdn_linear", dev, _p(x), _p(x_scale), _p(w), _p(w_scale), _p(bias),
-            _p(residual), _p(pre), _p(y), M, N, K, act_code, in_code, out_code, _p(workspace),
+    _launch(lib, "gdn_linear", dev, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias),
+            _ptr(residual), _ptr(pre), _ptr(y), M, N, K, act_code, in_code, out_code, _ptr(workspace),
             nbytes)
     return y, pre
 
@@ -1085,7 +1099,7 @@ def gdn_linear(x, w, bias=None, residual=None, act="none", out_dtype=None, x_sca
 def gdn_linear_bwd_workspace_size(M: int, N: int, K: int, act: str, in_dtype: torch.dtype,
                                   dy_dtype: torch.dtype) -> int:
     return int(load_library().gdn_linear_bwd_workspace_size(M, N, K, _act_code(act),
-                                                            _dt(in_dtype), _dt(dy_dtype)))
+                                                            _code(in_dtype), _code(dy_dtype)))
 
 
 def gdn_linear_bwd(dy, x, w, pre=None, act="none", want_dx=True, want_dw=True, want_dbias=True,
@@ -1098,14 +1112,14 @@ def gdn_linear_bwd(dy, x, w, pre=None, act="none", want_dx=True, want_dw=True, w
     lib = load_library()
     _need(x, "x")
     M, K = _rows_d(x, "x")
-    in_code = _dt(x.dtype)
+    in_code = _code(x.dtype)
     _need(w, "w", x.dtype)
     if w.dim() != 2 or w.shape[1] != K or w.shape[0] < 1:
         raise GdnError("w must be [N, %d], not %s" % (K, tuple(w.shape)))
     N = w.shape[0]
     _need(dy, "dy")
     _shape(dy, "dy", x.shape[:-1] + (N,))
-    dy_code = _dt(dy.dtype)
+    dy_code = _code(dy.dtype)
     act_code = _act_code(act)
     _like(pre, "pre", dy.shape, dy.dtype)
     if act_code and pre is None:
@@ -1125,8 +1139,8 @@ def gdn_linear_bwd(dy, x, w, pre=None, act="none", want_dx=True, want_dw=True, w
         dbias = torch.empty(N, dtype=torch.float32, device=dev)
     workspace, nbytes = _workspace(
         workspace, lib.gdn_linear_bwd_workspace_size(M, N, K, act_code, in_code, dy_code), dev)
-    _launch(lib, "gdn_linear_bwd", dev, _p(dy), _p(pre), _p(x), _p(w), _p(dx), _p(dw), _p(dbias),
-            M, N, K, act_code, in_code, dy_code, _p(workspace), nbytes)
+    _launch(lib, "gdn_linear_bwd", dev, _ptr(dy), _ptr(pre), _ptr(x), _ptr(w), _ptr(dx), _ptr(dw), _ptr(dbias),
+            M, N, K, act_code, in_code, dy_code, _ptr(workspace), nbytes)
     return dx, dw, dbias
 
 

@@ -40,12 +40,6 @@ __device__ __forceinline__ int seq_index(const int32_t *cu, int N, int64_t row) 
   return lo;
 }
 
-// Eight elements of type T as raw bits in registers (16 bytes for 16-bit
-// types, 32 for fp32).
-template <typename T>
-struct Raw8 {
-  u32x4 v[sizeof(T) / 2];
-};
 template <typename T>
 __device__ __forceinline__ Raw8<T> load_raw8(const T *p) {
   Raw8<T> r;
@@ -53,28 +47,6 @@ __device__ __forceinline__ Raw8<T> load_raw8(const T *p) {
   for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q)
     r.v[q] = reinterpret_cast<const u32x4 *>(p)[q];
   return r;
-}
-__device__ __forceinline__ void raw8_to_f32(const Raw8<float> &r, float *o) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[i] = __uint_as_float(r.v[0][i]);
-    o[4 + i] = __uint_as_float(r.v[1][i]);
-  }
-}
-__device__ __forceinline__ void raw8_to_f32(const Raw8<bf16_t> &r, float *o) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = __uint_as_float(r.v[0][i] << 16);
-    o[2 * i + 1] = __uint_as_float(r.v[0][i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void raw8_to_f32(const Raw8<_Float16> &r, float *o) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(r.v[0][i])));
-    o[2 * i + 1] =
-        static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(r.v[0][i] >> 16)));
-  }
 }
 
 constexpr int kFeRows = 64;   // rows per workgroup, streamed in order

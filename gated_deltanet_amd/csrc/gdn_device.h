@@ -124,27 +124,87 @@ struct Vec8<bf16_t> {
   }
 };
 
-// Elements e0 .. e0 + 7 of a row of d, zeros past the end. `vec`: d is a
-// multiple of 8, so that every group is whole and 16-byte aligned.
+// Eight elements of type T as raw bits in registers (16 bytes for 16-bit
+// types, 32 for fp32).
 template <typename T>
-__device__ __forceinline__ void load8(const T *row, int e0, int d, bool vec, float *o) {
-  if (vec) {
-    if (e0 < d) {
-      Vec8<T>::load(row + e0, o);
-      return;
-    }
+struct Raw8 {
+  u32x4 v[sizeof(T) / 2];
+};
+__device__ __forceinline__ void raw8_to_f32(const Raw8<float> &r, float *o) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    o[i] = __uint_as_float(r.v[0][i]);
+    o[4 + i] = __uint_as_float(r.v[1][i]);
+  }
+}
+__device__ __forceinline__ void raw8_to_f32(const Raw8<bf16_t> &r, float *o) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = e0 + i < d ? io<T>::to_f32(row[e0 + i]) : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = __uint_as_float(r.v[0][i] << 16);
+    o[2 * i + 1] = __uint_as_float(r.v[0][i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void raw8_to_f32(const Raw8<_Float16> &r, float *o) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(r.v[0][i])));
+    o[2 * i + 1] =
+        static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(r.v[0][i] >> 16)));
   }
 }
 
+// Elements e0 .. e0 + 7 of a row of d at any alignment of the element type,
+// zeros past the end. Whole groups are vector accesses (global memory takes
+// them at any address), so rows of a width that no vector divides run nearly as
+// fast; the row's last, partial group goes element by element.
 template <typename T>
-__device__ __forceinline__ void store8(T *row, int e0, int d, bool vec, const float *v) {
-  if (vec) {
-    if (e0 < d) Vec8<T>::store(row + e0, v);
+struct any_align {
+  typedef u32x4 vec __attribute__((aligned(2)));
+};
+template <>
+struct any_align<float> {
+  typedef u32x4 vec __attribute__((aligned(4)));
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T *row, int e0, int d) {
+  Raw8<T> r;
+  constexpr int Q = sizeof(T) / 2;
+  if (e0 + 8 <= d) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      r.v[q] = reinterpret_cast<const typename any_align<T>::vec *>(row + e0)[q];
+  } else {
+    constexpr int PER = 4 / sizeof(T);  // elements of a dword
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int h = 0; h < PER; ++h) {
+          const int e = e0 + (4 * q + w) * PER + h;
+          if (e >= d) continue;
+          if constexpr (sizeof(T) == 4) bits = __builtin_bit_cast(uint32_t, row[e]);
+          else bits |= static_cast<uint32_t>(__builtin_bit_cast(uint16_t, row[e])) << (16 * h);
+        }
+        r.v[q][w] = bits;
+      }
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *row, int e0, int d, float *o) {
+  raw8_to_f32(load_raw8(row, e0, d), o);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *row, int e0, int d, const float *v) {
+  if (e0 + 8 <= d) {
+    Raw8<T> r;
+    Vec8<T>::store(reinterpret_cast<T *>(&r), v);
+#pragma unroll
+    for (int q = 0; q < static_cast<int>(sizeof(T)) / 2; ++q)
+      reinterpret_cast<typename any_align<T>::vec *>(row + e0)[q] = r.v[q];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -165,11 +225,11 @@ __device__ __forceinline__ u32x2 to_e4m3(const float *v) {
 }
 
 template <>
-__device__ __forceinline__ void store8<e4m3_t>(e4m3_t *row, int e0, int d, bool vec,
-                                               const float *v) {
+__device__ __forceinline__ void store8<e4m3_t>(e4m3_t *row, int e0, int d, const float *v) {
+  typedef u32x2 vec __attribute__((aligned(1)));
   const u32x2 q = to_e4m3(v);
-  if (vec) {
-    if (e0 < d) *reinterpret_cast<u32x2 *>(row + e0) = q;
+  if (e0 + 8 <= d) {
+    *reinterpret_cast<vec *>(row + e0) = q;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

@@ -9,7 +9,9 @@
 // reduction axis (m or n contiguous, as w, x and du in the backward), with rows
 // a whole number of 16-byte vectors apart. Operands of other widths are first
 // copied into the workspace, padded with zeros.
+#include <cmath>
 #include <type_traits>
+#include <utility>
 
 #include "gdn_device.h"
 #include "gdn_internal.h"
@@ -20,7 +22,13 @@ namespace {
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kTile = 128;  // output tile of a workgroup
+// Most rows of rows_kernel; 16-bit weights above kFewRowsBytes half as many.
+// Against the tiles with a split reduction (us): bf16 4096 x 4096, 16 rows 9.5
+// and 12.5, 32 rows 13.1 and 13.5; bf16 4096 x 8192, 16 rows 18.4 and 18.2, 32
+// rows 24.1 and 18.4; e4m3 16384 x 4096, 32 rows 14.4 and 17.9; fp32 4096 x
+// 4096, 32 rows 25 and 40.
+constexpr int kFewRows = 32;
+constexpr int64_t kFewRowsBytes = int64_t{32} << 20;
 constexpr int kStep = 128;  // bytes of the reduction axis per step
 
 // ---------------------------------------------------------------------------
@@ -157,6 +165,16 @@ __device__ __forceinline__ void epilogue4(const Epilogue &e, int64_t m, int n, f
 // ---------------------------------------------------------------------------
 // tile kernel
 
+// f(0), f(1), .. f(N - 1) with constant arguments, whatever the code's size
+template <int... I, typename F>
+__device__ __forceinline__ void unrolled_(std::integer_sequence<int, I...>, F &&f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F &&f) {
+  unrolled_(std::make_integer_sequence<int, N>{}, f);
+}
+
 // eight e4m3 values as fp16
 __device__ __forceinline__ f16x8 widen_e4m3(uint32_t lo, uint32_t hi) {
   struct Quad {
@@ -170,10 +188,10 @@ __device__ __forceinline__ f16x8 widen_e4m3(uint32_t lo, uint32_t hi) {
 }
 
 // acc += A B over the 32 bytes of the reduction axis that the lane holds of
-// one operand row: two 16-byte vectors. The lanes lg = 0..3 of a row hold
-// bytes 16 lg and 64 + 16 lg of the 128-byte step; the matrix cores pair the
-// operands slot by slot, so any assignment of reduction indices to slots that
-// both operands share gives the product.
+// one operand row, two 16-byte vectors, in PIECES matrix instructions. The
+// lanes lg = 0..3 of a row hold bytes 16 lg and 64 + 16 lg of the 128-byte
+// step; the matrix cores pair the operands slot by slot, so any assignment of
+// reduction indices to slots that both operands share gives the product.
 //
 // The 8-bit matrix instructions take the products of a lane's 8 consecutive
 // bytes together, each cut off 13 bits below the largest's exponent (observed
@@ -182,44 +200,41 @@ __device__ __forceinline__ f16x8 widen_e4m3(uint32_t lo, uint32_t hi) {
 // not of an fp32 one. EXACT widens e4m3 to fp16 (which holds every e4m3
 // value) and uses the 16-bit instructions, whose sums are good to fp32.
 template <typename T, bool EXACT>
-__device__ __forceinline__ f32x4 mma_step(const u32x4 (&a)[2], const u32x4 (&b)[2], f32x4 acc) {
-  if constexpr (__is_same(T, bf16_t)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[h]),
-                                                    __builtin_bit_cast(bf16x8, b[h]), acc, 0, 0, 0);
-  } else if constexpr (__is_same(T, _Float16)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a[h]),
-                                                   __builtin_bit_cast(f16x8, b[h]), acc, 0, 0, 0);
-  } else if constexpr (__is_same(T, float)) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[h][i]),
-                                                   __uint_as_float(b[h][i]), acc, 0, 0, 0);
-  } else if constexpr (EXACT) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_e4m3(a[h][2 * q], a[h][2 * q + 1]),
-                                                     widen_e4m3(b[h][2 * q], b[h][2 * q + 1]), acc,
-                                                     0, 0, 0);
-  } else {
-    struct Pair {
-      u32x4 v[2];
-    };
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-        __builtin_bit_cast(i32x8, Pair{{a[0], a[1]}}), __builtin_bit_cast(i32x8, Pair{{b[0], b[1]}}),
-        acc, 0, 0, 0, 0, 0, 0);  // e4m3 by e4m3, no block scales
+struct Mma {
+  static constexpr int PIECES = __is_same(T, float) ? 8 : !__is_same(T, e4m3_t) ? 2 : EXACT ? 4 : 1;
+  __device__ static __forceinline__ f32x4 piece(const u32x4 (&a)[2], const u32x4 (&b)[2], f32x4 acc,
+                                                int p) {
+    if constexpr (__is_same(T, bf16_t)) {
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(bf16x8, a[p]), __builtin_bit_cast(bf16x8, b[p]), acc, 0, 0, 0);
+    } else if constexpr (__is_same(T, _Float16)) {
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a[p]),
+                                                    __builtin_bit_cast(f16x8, b[p]), acc, 0, 0, 0);
+    } else if constexpr (__is_same(T, float)) {
+      return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[p / 4][p % 4]),
+                                                  __uint_as_float(b[p / 4][p % 4]), acc, 0, 0, 0);
+    } else if constexpr (EXACT) {
+      const int q = 2 * (p % 2);
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(widen_e4m3(a[p / 2][q], a[p / 2][q + 1]),
+                                                    widen_e4m3(b[p / 2][q], b[p / 2][q + 1]), acc,
+                                                    0, 0, 0);
+    } else {
+      struct Pair {
+        u32x4 v[2];
+      };
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+          __builtin_bit_cast(i32x8, Pair{{a[0], a[1]}}),
+          __builtin_bit_cast(i32x8, Pair{{b[0], b[1]}}), acc, 0, 0, 0, 0, 0, 0);  // no block scales
+    }
   }
-  return acc;
-}
+  __device__ static __forceinline__ f32x4 step(const u32x4 (&a)[2], const u32x4 (&b)[2], f32x4 acc) {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) acc = piece(a, b, acc, p);
+    return acc;
+  }
+};
 
-// One matrix instruction of mma_step with the accumulator updated in place:
+// One matrix instruction of Mma with the accumulator updated in place:
 // part 0 or 1 (8-bit types have one part). Written in asm, with the
 // accumulator in the accumulation registers: from the builtins the compiler
 // moves accumulators between registers around a kernel that fills them all.
@@ -302,7 +317,7 @@ struct Operand {
   static constexpr int RB = BYRED ? TILE * ES : kStep;  // bytes of a row in LDS
   static constexpr int VPR = RB / 16;                // vectors of a row
   static constexpr int INDICES = kStep / ES;         // reduction indices of a stage
-  static constexpr int GROUPS = TILE == 256 ? 8 : 4;  // 16-row groups of a wave
+  static constexpr int GROUPS = TILE / 32;           // 16-row groups of a wave
 
   i32x4 rsrc;
   const char *base;
@@ -397,78 +412,186 @@ struct Operand {
   }
 };
 
-// One kTile x kTile tile of C (times one split of the reduction) per workgroup
-// of four waves, each 64 x 64 of it in 16 x 16 accumulators; the next stage is
-// in flight while one is multiplied.
-template <typename T, bool EXACT, bool PRED, bool QRED>
+// Epilogue of a wave's 16 G x 16 G of C, N a multiple of 4: the lane holds rows
+// m + 16 j, columns n + 16 i .. + 3. All of the residual and the scales are
+// requested first, so that their latency is paid once.
+template <typename TO, int ACT, int G>
+__device__ __forceinline__ void epilogue_tile_act(const Epilogue &e, f32x4 (&acc)[G][G], int64_t m,
+                                                  int n) {
+  typedef typename Vec4<TO>::raw raw;
+  raw res[G][G];
+  float xs[G];
+  f32x4 ws[G], b[G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    const int64_t row = m + 16 * j < e.M ? m + 16 * j : e.M - 1;
+    if (e.w_scale) xs[j] = e.x_scale[row];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (e.residual && n + 16 * i < e.N)
+        res[i][j] = *reinterpret_cast<const raw *>(static_cast<const TO *>(e.residual) +
+                                                   row * e.N + n + 16 * i);
+  }
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const bool in = n + 16 * i < e.N;
+    ws[i] = in && e.w_scale ? Vec4<float>::load(e.w_scale + n + 16 * i) : zero4();
+    b[i] = in && e.bias ? Vec4<float>::load(e.bias + n + 16 * i) : zero4();
+  }
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    if (m + 16 * j >= e.M) break;
+    const size_t at = static_cast<size_t>(m + 16 * j) * e.N + n;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      if (n + 16 * i >= e.N) break;
+      f32x4 v = acc[i][j];
+      if (e.w_scale) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] *= xs[j] * ws[i][k];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += b[i][k];
+      if (e.pre) Vec4<TO>::store(static_cast<TO *>(e.pre) + at + 16 * i, v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = act_fwd(v[k], ACT);
+      if (e.residual) {
+        const f32x4 x = __builtin_convertvector(res[i][j], f32x4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += x[k];
+      }
+      Vec4<TO>::store(static_cast<TO *>(e.y) + at + 16 * i, v);
+    }
+  }
+}
+template <typename TO, int G>
+__device__ __forceinline__ void epilogue_tile(const Epilogue &e, f32x4 (&acc)[G][G], int64_t m,
+                                              int n) {
+  switch (e.act) {
+    case 1: epilogue_tile_act<TO, 1>(e, acc, m, n); break;
+    case 2: epilogue_tile_act<TO, 2>(e, acc, m, n); break;
+    case 3: epilogue_tile_act<TO, 3>(e, acc, m, n); break;
+    default: epilogue_tile_act<TO, 0>(e, acc, m, n); break;
+  }
+}
+
+// One TILE x TILE tile of C (times one split of the reduction) per workgroup
+// of four waves, each a quarter of it in 16 x 16 accumulators. A wave reads the
+// fragments of the next step, and requests the stage NST steps ahead, between
+// the products of this one: read, multiplied and loaded one after the other a
+// step took 0.7 us with one workgroup a CU, three times its products' time. At
+// the barrier of step s, stage s + 1 has landed and stage s is fully read, so
+// the new stage goes over it.
+template <typename T, bool EXACT, bool PRED, bool QRED, int TILE, int NST>
 __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
-  constexpr int STAGE = 2 * kTile * kStep;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  constexpr int STAGE = 2 * TILE * kStep, G = TILE / 32;
+  __shared__ __attribute__((aligned(1024))) char smem[NST * STAGE];
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int lc = lane % 16, lg = lane / 16;
   const TileAt at = tile_at(g.tiles_m, g.tiles_n);
-  const int64_t m0 = at.m * kTile;
-  const int n0 = at.n * kTile;
-  const int wm = (wave / 2) * 64, wn = (wave % 2) * 64;
+  const int64_t m0 = at.m * TILE;
+  const int n0 = at.n * TILE;
+  const int wm = (wave / 2) * 16 * G, wn = (wave % 2) * 16 * G;
 
-  Operand<T, kTile, PRED> P;
-  Operand<T, kTile, QRED> Q;
+  Operand<T, TILE, PRED> P;
+  Operand<T, TILE, QRED> Q;
   P.init(g.p, g.ldp, m0, g.M, g.rbytes, g.red, lds_addr(smem), lane, wave, wm);
-  Q.init(g.q, g.ldq, n0, g.N, g.rbytes, g.red, lds_addr(smem) + kTile * kStep, lane, wave, wn);
+  Q.init(g.q, g.ldq, n0, g.N, g.rbytes, g.red, lds_addr(smem) + TILE * kStep, lane, wave, wn);
   const int s0 = blockIdx.y * g.steps;
   const int total = static_cast<int>((g.rbytes + kStep - 1) / kStep);
   const int s1 = s0 + g.steps < total ? s0 + g.steps : total;
-  auto issue = [&](int s, int buf) {
-    P.stage(s, true);
-    Q.stage(s, true);
-#pragma unroll
-    for (int i = 0; i < kTile / 32; ++i) {
-      P.load(i, buf * STAGE, wave);
-      Q.load(i, buf * STAGE, wave);
-    }
+  // load i of the stage set by next(), to buffer buf; past the split zeros are
+  // loaded (without traffic), so that as many loads are in flight at every step
+  constexpr int LOADS = 2 * G, READS = 4 * G;
+  auto next = [&](int s) {
+    P.stage(s, s < s1);
+    Q.stage(s, s < s1);
+  };
+  auto load = [&](int buf, int i) {
+    if (i % 2) Q.load(i / 2, buf * STAGE, wave);
+    else P.load(i / 2, buf * STAGE, wave);
+  };
+  struct Frags {
+    u32x4 a[G][2], b[G][2];
+  } F[2];
+  auto read = [&](Frags &f, int buf, int i) {
+    const int q = i / 4, h = i % 2;
+    if (i / 2 % 2) f.a[q][h] = __builtin_bit_cast(u32x4, Q.read(smem, buf * STAGE, q, h));
+    else f.b[q][h] = __builtin_bit_cast(u32x4, P.read(smem, buf * STAGE, q, h));
   };
 
-  f32x4 acc[4][4];  // [n tile][m tile]
+  f32x4 acc[G][G];  // [n tile][m tile]
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < G; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = zero4();
+    for (int j = 0; j < G; ++j) acc[i][j] = zero4();
 
-  if (s0 < s1) issue(s0, 0);
-  for (int s = s0; s < s1; ++s) {
-    const int buf = (s - s0) & 1;
-    wait_vmcnt<0>();
+  auto step = [&](int s, auto par) {
+    constexpr int B = decltype(par)::value;  // stage s % NST
+    const Frags &cur = F[B % 2];
+    Frags &nxt = F[(B + 1) % 2];
+    wait_vmcnt<(NST - 2) * LOADS>();
     wg_barrier();
-    if (s + 1 < s1) issue(s + 1, buf ^ 1);
-    u32x4 a[4][2], b[4][2];
+    next(s + NST);
+    constexpr int PIECES = Mma<T, EXACT>::PIECES, TOTAL = PIECES * G * G;
+    unrolled<TOTAL>([&](auto at_k) {
+      constexpr int k = decltype(at_k)::value;
+      constexpr int p = k / (G * G), i = k / G % G, j = k % G;
+      acc[i][j] = Mma<T, EXACT>::piece(cur.a[i], cur.b[j], acc[i][j], p);
+      constexpr int R0 = k * READS / TOTAL, L0 = k * LOADS / TOTAL;
+      unrolled<(k + 1) * READS / TOTAL - R0>(
+          [&](auto r) { read(nxt, (B + 1) % NST, R0 + decltype(r)::value); });
+      unrolled<(k + 1) * LOADS / TOTAL - L0>([&](auto r) { load(B, L0 + decltype(r)::value); });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  if (s0 < s1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int s = 0; s < NST; ++s) {
+      next(s0 + s);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        a[i][h] = __builtin_bit_cast(u32x4, Q.read(smem, buf * STAGE, i, h));
-        b[i][h] = __builtin_bit_cast(u32x4, P.read(smem, buf * STAGE, i, h));
+      for (int i = 0; i < LOADS; ++i) load(s, i);
+    }
+    wait_vmcnt<(NST - 1) * LOADS>();
+    wg_barrier();
+#pragma unroll
+    for (int i = 0; i < READS; ++i) read(F[0], 0, i);
+    // NST steps at a time; those past the end multiply zeros
+    for (int s = s0; s < s1; s += NST) {
+      step(s, std::integral_constant<int, 0>{});
+      step(s + 1, std::integral_constant<int, 1>{});
+      if constexpr (NST == 4) {
+        step(s + 2, std::integral_constant<int, 2>{});
+        step(s + 3, std::integral_constant<int, 3>{});
       }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mma_step<T, EXACT>(a[i], b[j], acc[i][j]);
+    }
+    wait_vmcnt<0>();  // no load may land in LDS that is no longer this workgroup's
   }
 
+  const int64_t m = m0 + wm + lc;
+  const int n = n0 + wn + 4 * lg;
+  if (g.part || g.N % 4 != 0) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t m = m0 + wm + 16 * j + lc;
-    if (m >= g.M) continue;
+    for (int j = 0; j < G; ++j) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + wn + 16 * i + 4 * lg;
-      if (n >= g.N) continue;
-      if (g.part)
-        *reinterpret_cast<f32x4 *>(g.part + (static_cast<size_t>(blockIdx.y) * g.M + m) * g.ldpart +
-                                   n) = acc[i][j];
-      else
-        epilogue4(g.e, m, n, acc[i][j]);
+      for (int i = 0; i < G; ++i) {
+        if (m + 16 * j >= g.M || n + 16 * i >= g.N) continue;
+        if (g.part)
+          *reinterpret_cast<f32x4 *>(g.part +
+                                     (static_cast<size_t>(blockIdx.y) * g.M + m + 16 * j) * g.ldpart +
+                                     n + 16 * i) = acc[i][j];
+        else
+          epilogue4(g.e, m + 16 * j, n + 16 * i, acc[i][j]);
+      }
     }
+  } else if (g.e.out_dtype == 1) {
+    epilogue_tile<bf16_t>(g.e, acc, m, n);
+  } else if (g.e.out_dtype == 2) {
+    epilogue_tile<_Float16>(g.e, acc, m, n);
+  } else {
+    epilogue_tile<float>(g.e, acc, m, n);
   }
 }
 
@@ -740,6 +863,71 @@ gemm256_kernel(const GemmArgs g) {
   }
 }
 
+// Few rows (decode): C is M <= 16 MT rows by 16 NT columns per workgroup, the
+// reduction dealt to its waves in steps of 128 bytes and joined in LDS. Every
+// weight byte goes to one wave only, so it is loaded straight to registers,
+// 8 KiB a wave in flight; x comes from the L2, once for the NT groups of
+// columns. Bound by the weights' HBM traffic.
+template <typename T, int MT, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void rows_kernel(const GemmArgs g) {
+  constexpr int AHEAD = 4 / NT;
+  __shared__ __attribute__((aligned(16))) float part[WAVES][MT * NT][64][4];
+  const int lane = threadIdx.x % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int lc = lane % 16, lg = lane / 16;
+  const int n0 = blockIdx.x * 16 * NT;
+  const int nrows = g.N - n0 < 16 * NT ? g.N - n0 : 16 * NT;
+  const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char *>(g.q + n0 * g.ldq), 0, static_cast<int>(nrows * g.ldq), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char *>(g.p), 0, static_cast<int>(g.M * g.ldp), 0x00020000);
+  const int total = static_cast<int>((g.rbytes + kStep - 1) / kStep);
+  f32x4 acc[NT][MT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[q][j] = zero4();
+  // rows past N or M, and bytes past the axis, read as zeros
+  auto fetch = [&](__amdgpu_buffer_rsrc_t from, int row, int64_t ld, uint32_t r) {
+    const uint32_t at = r < g.rbytes ? static_cast<uint32_t>(row * ld) + r : 0x80000000u;
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0));
+  };
+  for (int s = wave; s < total; s += WAVES * AHEAD) {
+    u32x4 w[AHEAD][NT][2], x[AHEAD][MT][2];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t r = (s + WAVES * i) * kStep + 64 * h + 16 * lg;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) w[i][q][h] = fetch(rq, 16 * q + lc, g.ldq, r);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) x[i][j][h] = fetch(rp, 16 * j + lc, g.ldp, r);
+      }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[q][j] = Mma<T, true>::step(w[i][q], x[i][j], acc[q][j]);
+  }
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+      *reinterpret_cast<f32x4 *>(part[wave][q * MT + j][lane]) = acc[q][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < NT * MT * 64; i += 64 * WAVES) {
+    const int t = i / 64, l = i % 64;
+    f32x4 v = *reinterpret_cast<const f32x4 *>(part[0][t][l]);
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k) v += *reinterpret_cast<const f32x4 *>(part[k][t][l]);
+    const int64_t m = 16 * (t % MT) + l % 16;
+    const int n = n0 + 16 * (t / MT) + 4 * (l / 16);
+    if (m < g.M && n < g.N) epilogue4(g.e, m, n, v);
+  }
+}
+
 // partial sums of the splits, added in order, through the epilogue
 __global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ part, int splits,
                                                    int64_t ldpart, const Epilogue e) {
@@ -773,14 +961,13 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const E *__restrict__ src
 // du[m][0 .. pitch) = dy act'(pre), zeros from N on (du may be null), and the
 // column sums of the unrounded du over each run of `run` rows (part may be
 // null). A workgroup owns 256 columns of one run: 8 columns of every eighth row
-// a thread. `vec`: N is a multiple of 8, so that the groups are whole vectors.
+// a thread.
 template <typename TG, typename T>
 __global__ __launch_bounds__(256) void du_kernel(const TG *__restrict__ dy,
                                                  const TG *__restrict__ pre, int64_t M, int N,
                                                  int act, T *__restrict__ du, int pitch, int run,
                                                  float *__restrict__ part) {
   __shared__ float s[8][257];
-  const bool vec = N % 8 == 0;
   const int g = threadIdx.x % 32, hi = threadIdx.x / 32;
   const int n = blockIdx.x * 256 + 8 * g;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * run;
@@ -789,19 +976,17 @@ __global__ __launch_bounds__(256) void du_kernel(const TG *__restrict__ dy,
 #pragma unroll 2
   for (int64_t m = m0 + hi; m < m1; m += 8) {
     float v[8];
-    load8(dy + m * N, n, N, vec, v);
+    load8(dy + m * N, n, N, v);
     if (act) {
       float u[8];
-      load8(pre + m * N, n, N, vec, u);
+      load8(pre + m * N, n, N, u);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= act_slope(u[i], act);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] += v[i];
-    if (du) {
-      // v is zero from N on (whatever act_slope gives there meets a zero dy)
-      store8(du + m * pitch, n, pitch, vec, v);
-    }
+    // v is zero from N on (whatever act_slope gives there meets a zero dy)
+    if (du) store8(du + m * pitch, n, pitch, v);
   }
   if (!part) return;
 #pragma unroll
@@ -832,9 +1017,9 @@ hipError_t with_type(int code, F &&f) {
   }
 }
 
-// One product: how the reduction is split and what that needs.
+// One product: the kernel, how the reduction is split and what that needs.
 struct GemmPlan {
-  int tile;
+  int tile;  // 0: rows_kernel
   int64_t tiles_m;
   int tiles_n;
   int splits, steps;
@@ -842,24 +1027,57 @@ struct GemmPlan {
   size_t part_bytes;
 };
 
-// Few output tiles leave CUs idle: the reduction is then split until about 256
-// workgroups run, each keeping at least four steps.
-GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes, bool large) {
-  GemmPlan p;
-  p.tile = large && M * N >= 64 * 256 * 256 ? 256 : kTile;
-  p.tiles_m = (M + p.tile - 1) / p.tile;
-  p.tiles_n = (N + p.tile - 1) / p.tile;
+// What a tile kernel costs in us on the whole card: start + rounds of 256
+// workgroups * (steps * step + tile), the last two less where part of the CUs
+// is idle; a split adds the joining pass. Fitted to timings (bf16, M x N x K,
+// us): 1024 x 4096 x 4096 128: 38, 256: 90; 4096 x 4096 x 4096 128: 145, 256:
+// 110; 4096 x 4096 x 1024 128: 60, 256: 43; 4096 x 2048 x 8192 128: 131, 256:
+// 166, 256 in two splits 123; 1024 x 1024 x 2048 128 in 1, 2, 4 splits: 19.3,
+// 16.4, 17.5; 4096 x 512 x 512 128 in 1, 2 splits 10.7, 19.5; fp32 2531 x 1000
+// x 520 64: 32, 128: 42. Results do not depend on the tile, but the order of a
+// split reduction's sums does on the splits.
+struct TileCost {
+  int tile;
+  float start, step, each;
+};
+constexpr TileCost kCost64F32{64, 7.0f, 0.55f, 3.0f}, kCost128F32{128, 7.0f, 2.0f, 6.0f},
+    kCost128{128, 7.0f, 0.44f, 6.0f}, kCost256{256, 4.0f, 1.4f, 18.0f};
+
+GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes, int es, bool large, bool by_rows) {
+  GemmPlan best{};
+  if (by_rows && M <= (es == 2 && N * rbytes > kFewRowsBytes ? kFewRows / 2 : kFewRows)) {
+    best.splits = best.steps = 1;
+    return best;
+  }
   const int total = static_cast<int>((rbytes + kStep - 1) / kStep);
-  const int64_t tiles = p.tiles_m * p.tiles_n;
-  int64_t want = tiles > 0 ? 256 / tiles : 1;
-  if (want > total / 4) want = total / 4;
-  if (want < 1) want = 1;
-  p.steps = static_cast<int>((total + want - 1) / want);
-  if (p.steps < 1) p.steps = 1;
-  p.splits = total > 0 ? (total + p.steps - 1) / p.steps : 1;
-  p.ldpart = (N + 3) / 4 * 4;
-  p.part_bytes = p.splits > 1 ? align256(static_cast<size_t>(p.splits) * M * p.ldpart * 4) : 0;
-  return p;
+  const TileCost cand[2] = {es == 4 ? kCost64F32 : kCost128, es == 4 ? kCost128F32 : kCost256};
+  float least = 0.0f;
+  for (int c = 0; c < (es == 4 || large ? 2 : 1); ++c) {
+    GemmPlan p;
+    p.tile = cand[c].tile;
+    p.tiles_m = (M + p.tile - 1) / p.tile;
+    p.tiles_n = (N + p.tile - 1) / p.tile;
+    const int64_t tiles = p.tiles_m * p.tiles_n;
+    for (int want = 1; want == 1 || (want * tiles <= 256 && want * 4 <= total); ++want) {
+      p.steps = (total + want - 1) / want;
+      if (p.steps < 1) p.steps = 1;
+      p.splits = total > 0 ? (total + p.steps - 1) / p.steps : 1;
+      const float full = static_cast<float>(tiles * p.splits) / 256.0f;
+      const float busy = full < 1.0f ? full : 1.0f;
+      const float rounds = full < 1.0f ? 1.0f : es == 4 ? full : std::ceil(full);
+      float cost = cand[c].start + rounds * (cand[c].step * p.steps * (0.7f + 0.3f * busy) +
+                                             cand[c].each * (0.35f + 0.65f * busy));
+      if (p.splits > 1) cost += 1.5f + 0.6e-6f * p.splits * M * N;
+      if (!best.tile || cost < least) {
+        best = p;
+        least = cost;
+      }
+    }
+  }
+  best.ldpart = (N + 3) / 4 * 4;
+  best.part_bytes =
+      best.splits > 1 ? align256(static_cast<size_t>(best.splits) * M * best.ldpart * 4) : 0;
+  return best;
 }
 
 // whether the large tile exists for the types: 16-bit and 8-bit matrix
@@ -872,8 +1090,28 @@ struct Matrix {
   bool by_red;  // the reduction axis is the slow one
 };
 
+// Column groups per workgroup: as many as leave every CU one; where even single
+// groups leave CUs idle, more waves share the reduction.
+template <typename T, int MT>
+hipError_t start_rows(const GemmArgs &g, hipStream_t stream) {
+  const int groups = (g.N + 15) / 16;
+  if (groups >= 4 * 256)
+    hipLaunchKernelGGL((rows_kernel<T, MT, 4, 8>), dim3((groups + 3) / 4), dim3(512), 0, stream, g);
+  else if (groups >= 2 * 256)
+    hipLaunchKernelGGL((rows_kernel<T, MT, 2, 8>), dim3((groups + 1) / 2), dim3(512), 0, stream, g);
+  else if (groups >= 128)
+    hipLaunchKernelGGL((rows_kernel<T, MT, 1, 8>), dim3(groups), dim3(512), 0, stream, g);
+  else
+    hipLaunchKernelGGL((rows_kernel<T, MT, 1, 16>), dim3(groups), dim3(1024), 0, stream, g);
+  return hipGetLastError();
+}
+
 template <typename T, bool EXACT, bool PRED, bool QRED>
 hipError_t start_gemm(const GemmArgs &g, const GemmPlan &p, hipStream_t stream) {
+  if constexpr (!PRED && !QRED) {
+    if (p.tile == 0)
+      return g.M <= 16 ? start_rows<T, 1>(g, stream) : start_rows<T, 2>(g, stream);
+  }
   const dim3 grid(static_cast<unsigned>(p.tiles_m * p.tiles_n), p.splits);
   if constexpr (!__is_same(T, float) && (!__is_same(T, e4m3_t) || !EXACT)) {
     if (p.tile == 256) {
@@ -881,7 +1119,14 @@ hipError_t start_gemm(const GemmArgs &g, const GemmPlan &p, hipStream_t stream) 
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((gemm_kernel<T, EXACT, PRED, QRED>), grid, dim3(256), 0, stream, g);
+  if constexpr (__is_same(T, float)) {
+    if (p.tile == 64)
+      hipLaunchKernelGGL((gemm_kernel<T, EXACT, PRED, QRED, 64, 2>), grid, dim3(256), 0, stream, g);
+    else
+      hipLaunchKernelGGL((gemm_kernel<T, EXACT, PRED, QRED, 128, 2>), grid, dim3(256), 0, stream, g);
+  } else {
+    hipLaunchKernelGGL((gemm_kernel<T, EXACT, PRED, QRED, 128, 4>), grid, dim3(256), 0, stream, g);
+  }
   return hipGetLastError();
 }
 
@@ -891,7 +1136,7 @@ hipError_t run_gemm(const Matrix &P, const Matrix &Q, int64_t M, int N, int64_t 
                     int dtype, const Epilogue &e, char *part, hipStream_t stream) {
   if (M == 0) return hipSuccess;
   const int64_t rbytes = pitch * esize(dtype);
-  const GemmPlan p = plan_gemm(M, N, rbytes, large_ok(dtype, e.out_dtype));
+  const GemmPlan p = plan_gemm(M, N, rbytes, esize(dtype), large_ok(dtype, e.out_dtype), !Q.by_red);
   GemmArgs g;
   g.p = static_cast<const char *>(P.p);
   g.q = static_cast<const char *>(Q.p);
@@ -964,8 +1209,8 @@ FwdLayout fwd_layout(int64_t M, int N, int K, int dtype) {
   L.w = off;
   if (L.pad) off += align256(static_cast<size_t>(N) * rb);
   L.part = off;
-  const size_t p1 = plan_gemm(M, N, rb, false).part_bytes;
-  const size_t p2 = plan_gemm(M, N, rb, large_ok(dtype, 1)).part_bytes;
+  const size_t p1 = plan_gemm(M, N, rb, es, false, true).part_bytes;
+  const size_t p2 = plan_gemm(M, N, rb, es, large_ok(dtype, 1), true).part_bytes;
   off += p1 > p2 ? p1 : p2;
   L.total = off;
   return L;
@@ -1005,8 +1250,8 @@ BwdLayoutL bwd_layout(int64_t M, int N, int K, int act, int in_dtype, int dy_dty
   off += align256(static_cast<size_t>((M + du_run(M) - 1) / du_run(M)) * N * 4);
   L.part = off;
   const bool large = large_ok(in_dtype, in_dtype);
-  const size_t p1 = plan_gemm(M, K, rn, large).part_bytes;
-  const size_t p2 = plan_gemm(N, K, M * es, large).part_bytes;
+  const size_t p1 = plan_gemm(M, K, rn, es, large, false).part_bytes;
+  const size_t p2 = plan_gemm(N, K, M * es, es, large, false).part_bytes;
   off += p1 > p2 ? p1 : p2;
   L.total = off;
   return L;

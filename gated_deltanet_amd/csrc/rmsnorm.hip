@@ -73,22 +73,21 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(const Norm
   const bool live = row0 < a.rows;
   const int64_t row = live ? row0 : a.rows - 1;
   const int d = a.d;
-  const bool vec = d % 8 == 0;
   const size_t base = static_cast<size_t>(row) * d;
 
   float v[kChunks][8];
 #pragma unroll
   for (int c = 0; c < kChunks; ++c)
-    load8(static_cast<const TI *>(a.x) + base, (c * NT + t) * 8, d, vec, v[c]);
+    load8(static_cast<const TI *>(a.x) + base, (c * NT + t) * 8, d, v[c]);
   if (NORM && a.residual) {
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       float s[8];
-      load8(static_cast<const TI *>(a.residual) + base, (c * NT + t) * 8, d, vec, s);
+      load8(static_cast<const TI *>(a.residual) + base, (c * NT + t) * 8, d, s);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] += s[i];
       if (a.r && live)
-        store8(static_cast<TI *>(a.r) + base, (c * NT + t) * 8, d, vec, v[c]);
+        store8(static_cast<TI *>(a.r) + base, (c * NT + t) * 8, d, v[c]);
     }
   }
   if constexpr (NORM) {
@@ -103,7 +102,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(const Norm
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       float w[8] = {};
-      if (a.norm_w) load8(a.norm_w, (c * NT + t) * 8, d, vec, w);
+      if (a.norm_w) load8(a.norm_w, (c * NT + t) * 8, d, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] * rs * (1.0f + w[i]);
     }
@@ -125,69 +124,100 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(const Norm
   if (!live) return;
 #pragma unroll
   for (int c = 0; c < kChunks; ++c)
-    store8(static_cast<TO *>(a.y) + base, (c * NT + t) * 8, d, vec, v[c]);
+    store8(static_cast<TO *>(a.y) + base, (c * NT + t) * 8, d, v[c]);
 }
 
 // Backward: a workgroup takes rows block, block + gridDim, ... (RPB of them at
-// a time) and keeps the weight gradient of its rows in registers; the
-// per-workgroup sums go to a.part [gridDim][d], added in order by
-// colsum_kernel.
-template <typename TI, typename TG, int NT>
+// a time, CH 8-element groups a thread) and keeps the weight gradient of its
+// rows in registers; the per-workgroup sums go to a.part [gridDim][d], added in
+// order by colsum_kernel. The next row is requested before this one is worked
+// on: without that, 2 us of latency a row left half of the bandwidth unused.
+// (Rows of 1024 threads have no registers for it, nor for the gain.)
+template <typename TI, typename TG, int NT, int CH>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
   constexpr int RPB = NT < 256 ? 256 / NT : 1;
+  constexpr bool AHEAD = NT < 1024;
   __shared__ float part[NT > 64 ? 2 * (NT / 64) : 1];
-  __shared__ float join[RPB > 1 ? RPB * NT * kChunks * 8 : 1];
+  __shared__ float join[RPB > 1 ? RPB * NT * CH * 8 : 1];
   const int t = threadIdx.x % NT, grp = threadIdx.x / NT;
   const int d = a.d;
-  const bool vec = d % 8 == 0;
-  float acc[kChunks][8] = {};
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * RPB; r0 < a.rows;
-       r0 += static_cast<int64_t>(gridDim.x) * RPB) {
+  float acc[CH][8] = {}, gain[AHEAD ? CH : 1][8];
+  auto load_gain = [&](int c, float *w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0.0f;
+    if (a.norm_w) load8(a.norm_w, (c * NT + t) * 8, d, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] += 1.0f;
+  };
+  struct Row {
+    Raw8<TI> r[CH], dr[CH];
+    Raw8<TG> dy[CH];
+  } now, ahead;
+  auto fetch = [&](int64_t r0, Row &row) {
+    const size_t base = static_cast<size_t>(r0 + grp < a.rows ? r0 + grp : a.rows - 1) * d;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int e0 = (c * NT + t) * 8;
+      row.r[c] = load_raw8(static_cast<const TI *>(a.r) + base, e0, d);
+      row.dy[c] = load_raw8(static_cast<const TG *>(a.dy) + base, e0, d);
+      if (a.dr) row.dr[c] = load_raw8(static_cast<const TI *>(a.dr) + base, e0, d);
+    }
+  };
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) load_gain(c, gain[c]);
+  }
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * RPB;
+  int64_t r0 = static_cast<int64_t>(blockIdx.x) * RPB;
+  if (AHEAD && r0 < a.rows) fetch(r0, ahead);
+  for (; r0 < a.rows; r0 += stride) {
     const bool live = r0 + grp < a.rows;
-    const size_t base = static_cast<size_t>(live ? r0 + grp : a.rows - 1) * d;
-    float r[kChunks][8], g[kChunks][8];
+    if constexpr (AHEAD) {
+      now = ahead;
+      if (r0 + stride < a.rows) fetch(r0 + stride, ahead);
+    } else {
+      fetch(r0, now);
+    }
     float sum[2] = {0.0f, 0.0f};  // sum r^2, sum g r
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int e0 = (c * NT + t) * 8;
-      load8(static_cast<const TI *>(a.r) + base, e0, d, vec, r[c]);
-      load8(static_cast<const TG *>(a.dy) + base, e0, d, vec, g[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      float w[8] = {};
-      if (a.norm_w) load8(a.norm_w, (c * NT + t) * 8, d, vec, w);
+    for (int c = 0; c < CH; ++c) {
+      float r[8], g[8], w[8];
+      raw8_to_f32(now.r[c], r);
+      raw8_to_f32(now.dy[c], g);
+      if constexpr (!AHEAD) load_gain(c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum[0] = fmaf(r[c][i], r[c][i], sum[0]);
-        sum[1] = fmaf(g[c][i] * (1.0f + w[i]), r[c][i], sum[1]);
+        sum[0] = fmaf(r[i], r[i], sum[0]);
+        sum[1] = fmaf(g[i] * (AHEAD ? gain[AHEAD ? c : 0][i] : w[i]), r[i], sum[1]);
       }
     }
     row_reduce<NT, 2, Add>(sum, part);
     const float rs = rsqrtf(sum[0] / static_cast<float>(d) + a.eps);
     const float along = rs * rs * sum[1] / static_cast<float>(d);
     if (live) {
+      const size_t base = static_cast<size_t>(r0 + grp) * d;
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int e0 = (c * NT + t) * 8;
-        float w[8] = {}, dx[8] = {};
-        if (a.norm_w) load8(a.norm_w, e0, d, vec, w);
-        if (a.dr) load8(static_cast<const TI *>(a.dr) + base, e0, d, vec, dx);
+      for (int c = 0; c < CH; ++c) {
+        float r[8], g[8], w[8], dx[8] = {};
+        raw8_to_f32(now.r[c], r);
+        raw8_to_f32(now.dy[c], g);
+        if constexpr (!AHEAD) load_gain(c, w);
+        if (a.dr) raw8_to_f32(now.dr[c], dx);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          acc[c][i] = fmaf(g[c][i], r[c][i] * rs, acc[c][i]);
-          dx[i] += rs * (g[c][i] * (1.0f + w[i]) - r[c][i] * along);
+          acc[c][i] = fmaf(g[i], r[i] * rs, acc[c][i]);
+          dx[i] += rs * (g[i] * (AHEAD ? gain[AHEAD ? c : 0][i] : w[i]) - r[i] * along);
         }
-        store8(static_cast<TI *>(a.dx) + base, e0, d, vec, dx);
+        store8(static_cast<TI *>(a.dx) + base, (c * NT + t) * 8, d, dx);
       }
     }
   }
   if (!a.part) return;
   float *out = a.part + static_cast<size_t>(blockIdx.x) * d;
   if constexpr (RPB > 1) {
-    constexpr int W = NT * kChunks * 8;
+    constexpr int W = NT * CH * 8;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) join[grp * W + (c * NT + t) * 8 + i] = acc[c][i];
     __syncthreads();
@@ -198,12 +228,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(const 
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = (c * NT + t) * 8 + i;
-        if (e < d) out[e] = acc[c][i];
-      }
+    for (int c = 0; c < CH; ++c) store8(out, (c * NT + t) * 8, d, acc[c]);
   }
 }
 
@@ -215,8 +240,10 @@ __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ 
   const int c = threadIdx.x % 32, g = threadIdx.x / 32;
   const int col = blockIdx.x * 32 + c;
   float v = 0.0f;
-  if (col < d)
+  if (col < d) {
+#pragma unroll 8
     for (int p = g; p < P; p += 32) v += part[static_cast<size_t>(p) * d + col];
+  }
   s[g][c] = v;
   __syncthreads();
   if (g == 0 && col < d) {
@@ -256,16 +283,34 @@ hipError_t launch_rows(const NormArgs &a) {
   });
 }
 
-// workgroups of the backward, and so partial sums of the weight gradient
+// the same for the backward: two 8-element groups a thread, four for the widest
+template <typename F>
+hipError_t with_threads_bwd(int d, F &&f) {
+  using std::integral_constant;
+  if (d <= 16 * 16) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  if (d <= 64 * 16) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (d <= 256 * 16) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (d <= 512 * 16) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  if (d <= 1024 * 16) return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+}
+
+// Workgroups of the backward, and so partial sums of the weight gradient: four
+// of 256 threads a CU, fewer for few rows, whose partial sums would cost as much
+// as the rows.
 int bwd_blocks(int64_t rows, int d) {
   int64_t b = 0;
-  with_threads(d, [&](auto nt) {
+  with_threads_bwd(d, [&](auto nt, auto) {
     constexpr int NT = decltype(nt)::value;
     constexpr int RPB = NT < 256 ? 256 / NT : 1;
-    b = (rows + RPB - 1) / RPB;
+    constexpr int64_t MOST = NT <= 256 ? 1024 : 1024 * 256 / NT;
+    const int64_t all = (rows + RPB - 1) / RPB;
+    b = all / 6;  // at least six rows a group, once every CU has a workgroup
+    if (b < 256) b = all < 256 ? all : 256;
+    if (b > MOST) b = MOST;
     return hipSuccess;
   });
-  return static_cast<int>(b < 512 ? b : 512);
+  return static_cast<int>(b);
 }
 
 }  // namespace
@@ -299,9 +344,9 @@ hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs &a) {
   if (P > 0) {
     const hipError_t e = with_type(a.in_dtype, [&](auto ti) {
       return with_type(a.dy_dtype, [&](auto tg) {
-        return with_threads(a.d, [&](auto nt) {
-          constexpr int NT = decltype(nt)::value;
-          hipLaunchKernelGGL((rmsnorm_bwd_kernel<decltype(ti), decltype(tg), NT>), dim3(P),
+        return with_threads_bwd(a.d, [&](auto nt, auto ch) {
+          constexpr int NT = decltype(nt)::value, CH = decltype(ch)::value;
+          hipLaunchKernelGGL((rmsnorm_bwd_kernel<decltype(ti), decltype(tg), NT, CH>), dim3(P),
                              dim3(NT < 256 ? 256 : NT), 0, a.stream, a);
           return hipGetLastError();
         });

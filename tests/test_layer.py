@@ -343,7 +343,9 @@ def test_linear(M, N, K, dtype, out):
 # a step, an odd number of steps, rows that no vector divides, a split reduction
 @gpu
 @pytest.mark.parametrize("M,N,K", [(2100, 2200, 328), (2100, 2201, 136), (4100, 1100, 64),
-                                   (2048, 2048, 4096), (2304, 2052, 24), (1900, 2500, 1155)])
+                                   (2048, 2048, 4096), (2304, 2052, 24), (1900, 2500, 1155),
+                                   (4000, 4000, 328), (3900, 4001, 136), (8100, 2000, 64),
+                                   (4096, 2048, 8192), (3840, 4052, 24), (4000, 4000, 1155)])
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f16", "f32"), ("e4m3", "bf16"),
                                        ("e4m3", "f16"), ("e4m3", "f32"), ("f32", "f32")])
 def test_linear_large_tiles(M, N, K, dtype, out):
@@ -353,7 +355,8 @@ def test_linear_large_tiles(M, N, K, dtype, out):
 
 
 @gpu
-@pytest.mark.parametrize("M,N,K", [(2100, 264, 2200), (2100, 2056, 1112), (512, 2100, 2100)])
+@pytest.mark.parametrize("M,N,K", [(2100, 264, 2200), (2100, 2056, 1112), (512, 2100, 2100),
+                                   (4000, 264, 4000), (512, 4000, 4000), (700, 4004, 3990)])
 @pytest.mark.parametrize("dtype,gtype,act", [("bf16", "bf16", "silu"), ("f16", "f16", "none"),
                                              ("bf16", "f32", "none"), ("f32", "f32", "none")])
 def test_linear_bwd_large_tiles(M, N, K, dtype, gtype, act):
