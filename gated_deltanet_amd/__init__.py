@@ -938,7 +938,7 @@ def _launch(lib, name, dev, *args):
     """Call a C entry point on dev's current stream, with dev current (kernels
     launch on the current device)."""
     fn = getattr(lib, name)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         # the stream's handle without a Stream object, 2 us a call cheaper
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
@@ -1086,9 +1086,9 @@ def gdn_linear(x, w, bias=None, residual=None, act="none", out_dtype=None, x_sca
     dev = _devices((x, "x"), (w, "w"), (x_scale, "x_scale"), (w_scale, "w_scale"), (bias, "bias"),
                    (residual, "residual"), (y, "y"), (pre, "pre"), (workspace, "workspace"))
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype, device=dev)
+        y = x.new_empty(shape, dtype=out_dtype)
     if pre is None and want_pre:
-        pre = torch.empty(shape, dtype=out_dtype, device=dev)
+        pre = torch.empty_like(y)
     workspace, nbytes = _workspace(workspace, lib.gdn_linear_workspace_size(M, N, K, in_code), dev)
     _launch(lib, "gdn_linear", dev, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias),
             _ptr(residual), _ptr(pre), _ptr(y), M, N, K, act_code, in_code, out_code, _ptr(workspace),

@@ -75,84 +75,74 @@ struct Vec4;
 template <>
 struct Vec4<float> {
   typedef f32x4 raw;
-  __device__ static __forceinline__ f32x4 load(const float *p) {
-    return *reinterpret_cast<const f32x4 *>(p);
-  }
-  __device__ static __forceinline__ void store(float *p, f32x4 v) {
-    *reinterpret_cast<f32x4 *>(p) = v;
-  }
+  typedef f32x4 mem __attribute__((aligned(4)));
 };
 template <>
 struct Vec4<_Float16> {
   typedef f16x4 raw;
-  __device__ static __forceinline__ f32x4 load(const _Float16 *p) {
-    return __builtin_convertvector(*reinterpret_cast<const f16x4 *>(p), f32x4);
-  }
-  __device__ static __forceinline__ void store(_Float16 *p, f32x4 v) {
-    *reinterpret_cast<f16x4 *>(p) = __builtin_convertvector(v, f16x4);
-  }
+  typedef f16x4 mem __attribute__((aligned(2)));
 };
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 template <>
 struct Vec4<bf16_t> {
   typedef bf16x4 raw;
-  __device__ static __forceinline__ f32x4 load(const bf16_t *p) {
-    return __builtin_convertvector(*reinterpret_cast<const bf16x4 *>(p), f32x4);
-  }
-  __device__ static __forceinline__ void store(bf16_t *p, f32x4 v) {
-    *reinterpret_cast<bf16x4 *>(p) = __builtin_convertvector(v, bf16x4);
-  }
+  typedef bf16x4 mem __attribute__((aligned(2)));
 };
 
-// four consecutive elements of a row; `whole`: all four exist and are aligned,
-// else the first cnt of them do
+// Four consecutive elements of a row at any alignment, or the first cnt < 4 of
+// them (then one by one).
 template <typename T>
-__device__ __forceinline__ f32x4 load4(const T *p, bool whole, int cnt) {
-  if (whole) return Vec4<T>::load(p);
-  f32x4 v = zero4();
+__device__ __forceinline__ typename Vec4<T>::raw load4_raw(const T *p, int cnt) {
+  if (cnt >= 4) return *reinterpret_cast<const typename Vec4<T>::mem *>(p);
+  typename Vec4<T>::raw v = __builtin_convertvector(zero4(), typename Vec4<T>::raw);
+  typedef decltype(v[0] + 0) any;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < cnt) v[i] = io<T>::to_f32(p[i]);
+  for (int i = 0; i < 3; ++i)
+    if (i < cnt) v[i] = static_cast<any>(io<T>::to_f32(p[i]));
   return v;
 }
 template <typename T>
-__device__ __forceinline__ void store4(T *p, f32x4 v, bool whole, int cnt) {
-  if (whole) {
-    Vec4<T>::store(p, v);
+__device__ __forceinline__ f32x4 load4(const T *p, int cnt) {
+  return __builtin_convertvector(load4_raw(p, cnt), f32x4);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T *p, f32x4 v, int cnt) {
+  if (cnt >= 4) {
+    *reinterpret_cast<typename Vec4<T>::mem *>(p) =
+        __builtin_convertvector(v, typename Vec4<T>::raw);
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 3; ++i)
     if (i < cnt) p[i] = io<T>::from_f32(v[i]);
 }
 
 template <typename TO>
 __device__ __forceinline__ void epilogue4_as(const Epilogue &e, int64_t m, int n, f32x4 v) {
-  const bool whole = e.N % 4 == 0;
   const int cnt = e.N - n;
   const size_t at = static_cast<size_t>(m) * e.N + n;
   if (e.w_scale) {
     const float xs = e.x_scale[m];
-    const f32x4 ws = load4(e.w_scale + n, whole, cnt);
+    const f32x4 ws = load4(e.w_scale + n, cnt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] *= xs * ws[i];
   }
   if (e.bias) {
-    const f32x4 b = load4(e.bias + n, whole, cnt);
+    const f32x4 b = load4(e.bias + n, cnt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += b[i];
   }
-  if (e.pre) store4(static_cast<TO *>(e.pre) + at, v, whole, cnt);
+  if (e.pre) store4(static_cast<TO *>(e.pre) + at, v, cnt);
   if (e.act) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = act_fwd(v[i], e.act);
   }
   if (e.residual) {
-    const f32x4 r = load4(static_cast<const TO *>(e.residual) + at, whole, cnt);
+    const f32x4 r = load4(static_cast<const TO *>(e.residual) + at, cnt);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] += r[i];
   }
-  store4(static_cast<TO *>(e.y) + at, v, whole, cnt);
+  store4(static_cast<TO *>(e.y) + at, v, cnt);
 }
 
 // u[m][n .. n + 3] (n a multiple of 4, m < M, n < N) through the epilogue
@@ -412,7 +402,7 @@ struct Operand {
   }
 };
 
-// Epilogue of a wave's 16 G x 16 G of C, N a multiple of 4: the lane holds rows
+// Epilogue of a wave's 16 G x 16 G of C: the lane holds rows
 // m + 16 j, columns n + 16 i .. + 3. All of the residual and the scales are
 // requested first, so that their latency is paid once.
 template <typename TO, int ACT, int G>
@@ -429,14 +419,14 @@ __device__ __forceinline__ void epilogue_tile_act(const Epilogue &e, f32x4 (&acc
 #pragma unroll
     for (int i = 0; i < G; ++i)
       if (e.residual && n + 16 * i < e.N)
-        res[i][j] = *reinterpret_cast<const raw *>(static_cast<const TO *>(e.residual) +
-                                                   row * e.N + n + 16 * i);
+        res[i][j] = load4_raw(static_cast<const TO *>(e.residual) + row * e.N + n + 16 * i,
+                              e.N - n - 16 * i);
   }
 #pragma unroll
   for (int i = 0; i < G; ++i) {
     const bool in = n + 16 * i < e.N;
-    ws[i] = in && e.w_scale ? Vec4<float>::load(e.w_scale + n + 16 * i) : zero4();
-    b[i] = in && e.bias ? Vec4<float>::load(e.bias + n + 16 * i) : zero4();
+    ws[i] = in && e.w_scale ? load4(e.w_scale + n + 16 * i, e.N - n - 16 * i) : zero4();
+    b[i] = in && e.bias ? load4(e.bias + n + 16 * i, e.N - n - 16 * i) : zero4();
   }
 #pragma unroll
   for (int j = 0; j < G; ++j) {
@@ -452,7 +442,7 @@ __device__ __forceinline__ void epilogue_tile_act(const Epilogue &e, f32x4 (&acc
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] += b[i][k];
-      if (e.pre) Vec4<TO>::store(static_cast<TO *>(e.pre) + at + 16 * i, v);
+      if (e.pre) store4(static_cast<TO *>(e.pre) + at + 16 * i, v, e.N - n - 16 * i);
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = act_fwd(v[k], ACT);
       if (e.residual) {
@@ -460,7 +450,7 @@ __device__ __forceinline__ void epilogue_tile_act(const Epilogue &e, f32x4 (&acc
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] += x[k];
       }
-      Vec4<TO>::store(static_cast<TO *>(e.y) + at + 16 * i, v);
+      store4(static_cast<TO *>(e.y) + at + 16 * i, v, e.N - n - 16 * i);
     }
   }
 }
@@ -572,20 +562,15 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs g) {
 
   const int64_t m = m0 + wm + lc;
   const int n = n0 + wn + 4 * lg;
-  if (g.part || g.N % 4 != 0) {
+  if (g.part) {
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
+    for (int j = 0; j < G; ++j)
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        if (m + 16 * j >= g.M || n + 16 * i >= g.N) continue;
-        if (g.part)
+      for (int i = 0; i < G; ++i)
+        if (m + 16 * j < g.M && n + 16 * i < g.N)
           *reinterpret_cast<f32x4 *>(g.part +
                                      (static_cast<size_t>(blockIdx.y) * g.M + m + 16 * j) * g.ldpart +
                                      n + 16 * i) = acc[i][j];
-        else
-          epilogue4(g.e, m + 16 * j, n + 16 * i, acc[i][j]);
-      }
-    }
   } else if (g.e.out_dtype == 1) {
     epilogue_tile<bf16_t>(g.e, acc, m, n);
   } else if (g.e.out_dtype == 2) {
@@ -621,7 +606,7 @@ __device__ __forceinline__ void epilogue_rows8(const Epilogue &e, const float *r
     for (int i = 0; i < 4; ++i) v[r][i] += b[i];
     if (e.pre) {
       TO *to = static_cast<TO *>(e.pre) + (m + r) * e.N;
-      Vec4<TO>::store(to + n, v[r]);
+      store4(to + n, v[r], e.N - n);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[r][i] = act_fwd(v[r][i], ACT);
@@ -631,23 +616,23 @@ __device__ __forceinline__ void epilogue_rows8(const Epilogue &e, const float *r
       for (int i = 0; i < 4; ++i) v[r][i] += x[i];
     }
     TO *to = static_cast<TO *>(e.y) + (m + r) * e.N;
-    Vec4<TO>::store(to + n, v[r]);
+    store4(to + n, v[r], e.N - n);
     // an activation's rows one after the other: side by side they would spill
     if (ACT) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// Epilogue of one wave's part of a tile, N a multiple of 4: `halves` times 32
-// rows, from row m + hstep * half, staged to LDS at `rows` by stage(half). The
-// residual of 8 rows is requested while the 8 before them are worked on.
+// Epilogue of one wave's part of a tile: twice 32 rows, from row
+// m + hstep * half, staged to LDS at `rows` by stage(half). The
+// residual of 8 rows is requested two groups of 8 ahead.
 template <typename TO, typename F>
 __device__ __forceinline__ void epilogue_wave(const Epilogue &e, const float *rows, int ldc,
                                               int64_t m, int hstep, int n, F &&stage) {
   typedef typename Vec4<TO>::raw raw;
   const bool in = n < e.N;
   f32x4 ws = zero4(), b = zero4();
-  if (in && e.w_scale) ws = Vec4<float>::load(e.w_scale + n);
-  if (in && e.bias) b = Vec4<float>::load(e.bias + n);
+  if (in && e.w_scale) ws = load4(e.w_scale + n, e.N - n);
+  if (in && e.bias) b = load4(e.bias + n, e.N - n);
   // x_scale of row r of half h in lane 32 h + r
   float xs = 0.0f;
   if (e.w_scale) {
@@ -655,27 +640,36 @@ __device__ __forceinline__ void epilogue_wave(const Epilogue &e, const float *ro
     const int64_t row = m + hstep * (lane / 32) + lane % 32;
     xs = e.x_scale[row < e.M ? row : e.M - 1];
   }
-  raw res[8], next[8];
-  auto fetch = [&](int64_t at) {
-    if (!e.residual || !in) return;
+  // the residual of the 8 rows at hand and of the next two groups of 8
+  raw res[8], next[8], after[8];
+  auto fetch = [&](int group) {  // 0 .. 7: four groups per half
+    if (!e.residual || !in || group >= 8) return;
+    const int64_t at = m + hstep * (group / 4) + 8 * (group % 4);
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int64_t row = at + r < e.M ? at + r : e.M - 1;
       const TO *from = static_cast<const TO *>(e.residual) + row * e.N;
-      next[r] = *reinterpret_cast<const raw *>(from + n);
+      after[r] = load4_raw(from + n, e.N - n);
     }
   };
-  fetch(m);
+  auto shift = [&]() {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      res[r] = next[r];
+      next[r] = after[r];
+    }
+  };
+  fetch(0);
+  shift();
+  fetch(1);
 #pragma unroll 1
   for (int half = 0; half < 2; ++half) {
     stage(half);
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       const int64_t at = m + hstep * half + 8 * q;
-#pragma unroll
-      for (int r = 0; r < 8; ++r) res[r] = next[r];
-      if (q < 3) fetch(at + 8);
-      else if (half == 0) fetch(m + hstep);
+      shift();
+      fetch(4 * half + q + 2);
       if (!in) continue;
       const float *from = rows + 8 * q * ldc;
       const int xl = 32 * half + 8 * q;
@@ -843,16 +837,16 @@ gemm256_kernel(const GemmArgs g) {
   const int n = n0 + 4 * lane;
   const int64_t m = m0 + (wave / 2) * 128 + (wave % 2) * 32;  // row of `rows`, + 64 in half 1
   const float *rows = cs + 32 * wave * LDC + 4 * lane;
-  if (g.part || g.N % 4 != 0) {
+  if (g.part) {
     for (int half = 0; half < 2; ++half) {
       stage(half);
       if (n >= g.N) continue;
       float *out = g.part + (static_cast<size_t>(blockIdx.y) * g.M + m + 64 * half) * g.ldpart + n;
-      for (int r = 0; r < 32 && m + 64 * half + r < g.M; ++r) {
-        const f32x4 v = *reinterpret_cast<const f32x4 *>(rows + r * LDC);
-        if (g.part) *reinterpret_cast<f32x4 *>(out + r * g.ldpart) = v;
-        else epilogue4(g.e, m + 64 * half + r, n, v);
-      }
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r)
+        if (m + 64 * half + r < g.M)
+          *reinterpret_cast<f32x4 *>(out + r * g.ldpart) =
+              *reinterpret_cast<const f32x4 *>(rows + r * LDC);
     }
   } else if (g.e.out_dtype == 1) {
     epilogue_wave<bf16_t>(g.e, rows, LDC, m, 64, n, stage);
@@ -945,16 +939,26 @@ __global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ par
 // ---------------------------------------------------------------------------
 // operand layout
 
-// dst[r][0 .. pitch) = src[r][0 .. cols) and zeros (E: raw bits of an element)
+// dst[r][0 .. pitch) = src[r][0 .. cols) and zeros (E: raw bits of an element):
+// a wave takes rows, a lane their 16-byte vectors, read at any alignment
 template <typename E>
 __global__ __launch_bounds__(256) void pad_rows_kernel(const E *__restrict__ src, int64_t rows,
                                                        int cols, E *__restrict__ dst, int pitch) {
-  const int64_t total = rows * pitch;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = i / pitch;
-    const int c = static_cast<int>(i % pitch);
-    dst[i] = c < cols ? src[r * cols + c] : E(0);
+  constexpr int PER = 16 / sizeof(E);
+  typedef u32x4 any __attribute__((aligned(1)));
+  const int lane = threadIdx.x % 64;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 64; r < rows;
+       r += static_cast<int64_t>(gridDim.x) * 4) {
+    const E *from = src + r * cols;
+    E *to = dst + r * pitch;
+#pragma unroll 4
+    for (int c = lane * PER; c < pitch; c += 64 * PER) {
+      if (c + PER <= cols) {
+        *reinterpret_cast<u32x4 *>(to + c) = *reinterpret_cast<const any *>(from + c);
+      } else {
+        for (int i = 0; i < PER; ++i) to[c + i] = c + i < cols ? from[c + i] : E(0);
+      }
+    }
   }
 }
 
@@ -1058,7 +1062,10 @@ GemmPlan plan_gemm(int64_t M, int N, int64_t rbytes, int es, bool large, bool by
     p.tiles_m = (M + p.tile - 1) / p.tile;
     p.tiles_n = (N + p.tile - 1) / p.tile;
     const int64_t tiles = p.tiles_m * p.tiles_n;
-    for (int want = 1; want == 1 || (want * tiles <= 256 && want * 4 <= total); ++want) {
+    // 1, 2, 3, 4, 6, 8, 12, .. splits while they leave no more workgroups than
+    // CUs, nor fewer than four steps each
+    for (int want = 1; want == 1 || (want * tiles <= 256 && want * 4 <= total);
+         want += want < 4 ? 1 : want % 3 ? want / 2 : want / 3) {
       p.steps = (total + want - 1) / want;
       if (p.steps < 1) p.steps = 1;
       p.splits = total > 0 ? (total + p.steps - 1) / p.steps : 1;
@@ -1180,10 +1187,10 @@ void by_size(int es, F &&f) {
 
 hipError_t pad_rows(const void *src, int64_t rows, int cols, void *dst, int pitch, int es,
                     hipStream_t stream) {
-  const int64_t blocks = (rows * pitch + 1023) / 1024;
+  const int64_t blocks = (rows + 3) / 4;
   by_size(es, [&](auto e) {
     using E = decltype(e);
-    hipLaunchKernelGGL(pad_rows_kernel<E>, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)),
+    hipLaunchKernelGGL(pad_rows_kernel<E>, dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)),
                        dim3(256), 0, stream, static_cast<const E *>(src), rows, cols,
                        static_cast<E *>(dst), pitch);
   });
@@ -1209,8 +1216,9 @@ FwdLayout fwd_layout(int64_t M, int N, int K, int dtype) {
   L.w = off;
   if (L.pad) off += align256(static_cast<size_t>(N) * rb);
   L.part = off;
-  const size_t p1 = plan_gemm(M, N, rb, es, false, true).part_bytes;
-  const size_t p2 = plan_gemm(M, N, rb, es, large_ok(dtype, 1), true).part_bytes;
+  // e4m3 inputs: whichever of the tiles for 16-bit and fp32 outputs needs more
+  const size_t p1 = plan_gemm(M, N, rb, es, large_ok(dtype, 1), true).part_bytes;
+  const size_t p2 = dtype == kE4m3 ? plan_gemm(M, N, rb, es, false, true).part_bytes : 0;
   off += p1 > p2 ? p1 : p2;
   L.total = off;
   return L;
@@ -1292,7 +1300,8 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a) {
   const int run = du_run(a.M);
   const int runs = static_cast<int>((a.M + run - 1) / run);
   const void *du = L.own_du ? a.ws + L.du : a.dy;
-  float *db = reinterpret_cast<float *>(a.ws + L.db);
+  // a single run's sums are dbias itself
+  float *db = runs == 1 ? a.dbias : reinterpret_cast<float *>(a.ws + L.db);
   hipError_t err = hipSuccess;
   if (a.M > 0 && (L.own_du || a.dbias)) {
     err = with_type(a.in_dtype, [&](auto t) {
@@ -1309,7 +1318,7 @@ hipError_t launch_linear_bwd(const LinearBwdArgs &a) {
     });
     if (err != hipSuccess) return err;
   }
-  if (a.dbias) {
+  if (a.dbias && runs != 1) {
     err = launch_colsum(db, runs, a.N, a.dbias, a.stream);
     if (err != hipSuccess) return err;
   }
