@@ -1227,7 +1227,7 @@ FwdLayout fwd_layout(int64_t M, int N, int K, int dtype) {
 constexpr int kDuRuns = 256;  // most runs of rows whose column sums are kept
 int du_run(int64_t M) {
   const int64_t r = (M + kDuRuns - 1) / kDuRuns;
-  return static_cast<int>(r < 64 ? 64 : r);
+  return static_cast<int>(r < 16 ? 16 : r);
 }
 
 // backward workspace: du (when it is not dy itself), padded copies of x and w

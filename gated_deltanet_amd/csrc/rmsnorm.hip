@@ -62,11 +62,12 @@ __device__ __forceinline__ void row_reduce(float (&v)[K], float *part) {
   }
 }
 
-// NT threads own a row; a workgroup of max(NT, 256) threads owns one or more.
+// NT threads own a row: a workgroup of its own, or 256 / NT rows of one wave or
+// less each share one.
 // NORM false: y = x (the row quantiser).
 template <typename TI, typename TO, int NT, bool NORM>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(const NormArgs a) {
-  constexpr int RPB = NT < 256 ? 256 / NT : 1;
+__global__ __launch_bounds__(NT <= 64 ? 256 : NT) void rmsnorm_kernel(const NormArgs a) {
+  constexpr int RPB = NT <= 64 ? 256 / NT : 1;
   __shared__ float part[NT > 64 ? NT / 64 : 1];
   const int t = threadIdx.x % NT;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / NT;
@@ -134,8 +135,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(const Norm
 // on: without that, 2 us of latency a row left half of the bandwidth unused.
 // (Rows of 1024 threads have no registers for it, nor for the gain.)
 template <typename TI, typename TG, int NT, int CH>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  constexpr int RPB = NT < 256 ? 256 / NT : 1;
+__global__ __launch_bounds__(NT <= 64 ? 256 : NT) void rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  constexpr int RPB = NT <= 64 ? 256 / NT : 1;
   constexpr bool AHEAD = NT < 1024;
   __shared__ float part[NT > 64 ? 2 * (NT / 64) : 1];
   __shared__ float join[RPB > 1 ? RPB * NT * CH * 8 : 1];
@@ -232,22 +233,23 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(const 
   }
 }
 
-// out[c] = sum over p of part[p][c], in order: 32 columns per workgroup, the
-// rows dealt to 32 groups of threads and joined in a fixed tree
+// out[c] = sum over p of part[p][c], in order: 16 columns per workgroup, the
+// rows dealt to 64 groups of threads and joined in order
 __global__ __launch_bounds__(1024) void colsum_kernel(const float *__restrict__ part, int P, int d,
                                                       float *__restrict__ out) {
-  __shared__ float s[32][33];
-  const int c = threadIdx.x % 32, g = threadIdx.x / 32;
-  const int col = blockIdx.x * 32 + c;
+  __shared__ float s[64][17];
+  const int c = threadIdx.x % 16, g = threadIdx.x / 16;
+  const int col = blockIdx.x * 16 + c;
   float v = 0.0f;
   if (col < d) {
 #pragma unroll 8
-    for (int p = g; p < P; p += 32) v += part[static_cast<size_t>(p) * d + col];
+    for (int p = g; p < P; p += 64) v += part[static_cast<size_t>(p) * d + col];
   }
   s[g][c] = v;
   __syncthreads();
   if (g == 0 && col < d) {
-    for (int q = 1; q < 32; ++q) v += s[q][c];
+#pragma unroll
+    for (int q = 1; q < 64; ++q) v += s[q][c];
     out[col] = v;
   }
 }
@@ -275,10 +277,10 @@ template <bool NORM, typename TI, typename TO>
 hipError_t launch_rows(const NormArgs &a) {
   return with_threads(a.d, [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
-    constexpr int RPB = NT < 256 ? 256 / NT : 1;
+    constexpr int RPB = NT <= 64 ? 256 / NT : 1;
     hipLaunchKernelGGL((rmsnorm_kernel<TI, TO, NT, NORM>),
                        dim3(static_cast<unsigned>((a.rows + RPB - 1) / RPB)),
-                       dim3(NT < 256 ? 256 : NT), 0, a.stream, a);
+                       dim3(NT <= 64 ? 256 : NT), 0, a.stream, a);
     return hipGetLastError();
   });
 }
@@ -289,23 +291,24 @@ hipError_t with_threads_bwd(int d, F &&f) {
   using std::integral_constant;
   if (d <= 16 * 16) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
   if (d <= 64 * 16) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (d <= 128 * 16) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
   if (d <= 256 * 16) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
   if (d <= 512 * 16) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
   if (d <= 1024 * 16) return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
   return f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
-// Workgroups of the backward, and so partial sums of the weight gradient: four
-// of 256 threads a CU, fewer for few rows, whose partial sums would cost as much
-// as the rows.
+// Workgroups of the backward, and so partial sums of the weight gradient: 1024
+// threads a CU (16384 x 4096 bf16: 115 us with 1024 workgroups, 120 with 512),
+// fewer for few rows, whose partial sums would cost as much as the rows.
 int bwd_blocks(int64_t rows, int d) {
   int64_t b = 0;
   with_threads_bwd(d, [&](auto nt, auto) {
     constexpr int NT = decltype(nt)::value;
-    constexpr int RPB = NT < 256 ? 256 / NT : 1;
+    constexpr int RPB = NT <= 64 ? 256 / NT : 1;
     constexpr int64_t MOST = NT <= 256 ? 1024 : 1024 * 256 / NT;
     const int64_t all = (rows + RPB - 1) / RPB;
-    b = all / 6;  // at least six rows a group, once every CU has a workgroup
+    b = all / 2;  // at least two rows a group, once every CU has a workgroup
     if (b < 256) b = all < 256 ? all : 256;
     if (b > MOST) b = MOST;
     return hipSuccess;
@@ -316,7 +319,7 @@ int bwd_blocks(int64_t rows, int d) {
 }  // namespace
 
 hipError_t launch_colsum(const float *part, int P, int d, float *out, hipStream_t stream) {
-  hipLaunchKernelGGL(colsum_kernel, dim3((d + 31) / 32), dim3(1024), 0, stream, part, P, d, out);
+  hipLaunchKernelGGL(colsum_kernel, dim3((d + 15) / 16), dim3(1024), 0, stream, part, P, d, out);
   return hipGetLastError();
 }
 
@@ -347,7 +350,7 @@ hipError_t launch_add_rmsnorm_bwd(const NormBwdArgs &a) {
         return with_threads_bwd(a.d, [&](auto nt, auto ch) {
           constexpr int NT = decltype(nt)::value, CH = decltype(ch)::value;
           hipLaunchKernelGGL((rmsnorm_bwd_kernel<decltype(ti), decltype(tg), NT, CH>), dim3(P),
-                             dim3(NT < 256 ? 256 : NT), 0, a.stream, a);
+                             dim3(NT <= 64 ? 256 : NT), 0, a.stream, a);
           return hipGetLastError();
         });
       });
