@@ -596,32 +596,50 @@ __device__ __forceinline__ void epilogue_rows8(const Epilogue &e, const float *r
   f32x4 v[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r) v[r] = *reinterpret_cast<const f32x4 *>(rows + r * ldc);
+  // one branch a step for all rows: branches in every row took twice the time
+  if (e.w_scale) {
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if (m + r >= e.M) break;
-    if (e.w_scale) {
+    for (int r = 0; r < 8; ++r) {
       const float x = readlane(xs, xlane + r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[r][i] *= x * ws[i];
     }
+  }
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[r][i] += b[i];
-    if (e.pre) {
-      TO *to = static_cast<TO *>(e.pre) + (m + r) * e.N;
-      store4(to + n, v[r], e.N - n);
-    }
+  const int cnt = e.N - n, left = e.M - m < 8 ? static_cast<int>(e.M - m) : 8;
+  auto store_rows = [&](void *out) {
+    TO *to = static_cast<TO *>(out) + m * e.N;
+    if (left == 8 && cnt >= 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[r][i] = act_fwd(v[r][i], ACT);
-    if (e.residual) {
+      for (int r = 0; r < 8; ++r, to += e.N) store4(to + n, v[r], 4);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r, to += e.N)
+        if (r < left) store4(to + n, v[r], cnt);
+    }
+  };
+  if (e.pre) store_rows(e.pre);
+  if (ACT) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[r][i] = act_fwd(v[r][i], ACT);
+      // two rows at a time: more side by side would spill
+      if (r % 2) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (e.residual) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
       const f32x4 x = __builtin_convertvector(res[r], f32x4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[r][i] += x[i];
     }
-    TO *to = static_cast<TO *>(e.y) + (m + r) * e.N;
-    store4(to + n, v[r], e.N - n);
-    // an activation's rows one after the other: side by side they would spill
-    if (ACT) __builtin_amdgcn_sched_barrier(0);
   }
+  store_rows(e.y);
 }
 
 // Epilogue of one wave's part of a tile: twice 32 rows, from row
@@ -647,11 +665,16 @@ __device__ __forceinline__ void epilogue_wave(const Epilogue &e, const float *ro
   auto fetch = [&](int group) {  // 0 .. 7: four groups per half
     if (!e.residual || !in || group >= 8) return;
     const int64_t at = m + hstep * (group / 4) + 8 * (group % 4);
+    const TO *from[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int64_t row = at + r < e.M ? at + r : e.M - 1;
-      const TO *from = static_cast<const TO *>(e.residual) + row * e.N;
-      after[r] = load4_raw(from + n, e.N - n);
+    for (int r = 0; r < 8; ++r)
+      from[r] = static_cast<const TO *>(e.residual) + (at + r < e.M ? at + r : e.M - 1) * e.N;
+    if (e.N - n >= 4) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) after[r] = load4_raw(from[r] + n, 4);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) after[r] = load4_raw(from[r] + n, e.N - n);
     }
   };
   auto shift = [&]() {
@@ -710,8 +733,8 @@ __device__ __forceinline__ void store_half(uint32_t to, const f32x4 (&acc)[8][8]
 // where ' is the next step, whose Bf is this one's Bs. At the barrier the next
 // stage has landed and this one is fully read: the stage after next is loaded
 // over it, a whole step (about 1 us) ahead of its use. Measured: M16384 N8192
-// K2048 bf16 with bias and silu 527 us (1.04 PFLOP/s; products alone 390 us),
-// M16384 N4096 K4096 e4m3 with residual 266 us (2.07 PFLOP/s; alone 170 us):
+// K2048 bf16 with bias and silu 482 us (1.14 PFLOP/s; products alone 390 us),
+// M16384 N4096 K4096 e4m3 with residual 250 us (2.20 PFLOP/s; alone 170 us):
 // bound by the matrix cores, then by the epilogue, in which they rest.
 struct Half {
   i32x8 v[4];
